@@ -36,6 +36,10 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 HISA_KEY_BF16, HISA_KEY_E4M3 = 0, 1
+HISA_CACHE_BF16, HISA_CACHE_FP4 = 0, 1
+HISA_ROPE_MAX_PAIRS = 128
+HISA_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+HISA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 HISA_POOL_MEAN, HISA_POOL_MAX = 0, 1
 HISA_OK, HISA_E_INVAL, HISA_E_UNSUPPORTED, HISA_E_WORKSPACE, HISA_E_CUDA = range(5)
 HISA_E_SCRATCH_LIMIT = 5
@@ -50,9 +54,12 @@ EXPORTS = ("hisa_pool_blocks", "hisa_append", "hisa_select_workspace_bytes", "hi
            "hisa_cp_tokens", "hisa_merge_topk", "hisa_sparse_attn_workspace_bytes", "hisa_sparse_attn",
            "dsa_flat_workspace_bytes", "dsa_flat_select", "hisa_topk_f32",
            "hisa_profile_enable", "hisa_profile_read", "hisa_status_string", "hisa_last_cuda_error",
-           "hisa_selftest_wait")
+           "hisa_selftest_wait",
+           "hisa_select_blocks_workspace_bytes", "hisa_select_blocks", "hisa_rope_init", "hisa_rope",
+           "hisa_cache_store", "hisa_cache_load", "hisa_block_attn_workspace_bytes", "hisa_block_attn")
 PHASES = ("block_score", "block_select", "token_score", "token_select", "flat_score",
-          "flat_select", "pool", "append", "topk", "qsplit", "merge", "attn")
+          "flat_select", "pool", "append", "topk", "qsplit", "merge", "attn",
+          "rope", "cache", "block_attn")
 
 
 class hisa_kv(ctypes.Structure):
@@ -61,6 +68,20 @@ class hisa_kv(ctypes.Structure):
                 ("len", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("batch", ctypes.c_int32), ("cap", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("B", ctypes.c_int32), ("dtype", ctypes.c_int32), ("pool", ctypes.c_int32)]
+
+
+class hisa_attn_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("len", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("cap", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_mul", ctypes.c_float),
+                ("v_mul", ctypes.c_float)]
+
+
+class hisa_rope_plan(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("off", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("gain", ctypes.c_float), ("ready", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * HISA_ROPE_MAX_PAIRS)]
 
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -95,6 +116,18 @@ _lib.hisa_sparse_attn_workspace_bytes.argtypes = [_I, _I]
 _lib.hisa_sparse_attn_workspace_bytes.restype = _Z
 _lib.hisa_sparse_attn.argtypes = [_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, ctypes.c_float, _P, _P,
                                   _P, _P, _Z, _P]
+_D, _F = ctypes.c_double, ctypes.c_float
+_AKVP, _RPP = ctypes.POINTER(hisa_attn_kv), ctypes.POINTER(hisa_rope_plan)
+_lib.hisa_select_blocks_workspace_bytes.argtypes = [_KVP, _I, _I, _I]
+_lib.hisa_select_blocks_workspace_bytes.restype = _Z
+_lib.hisa_select_blocks.argtypes = [_KVP, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]
+_lib.hisa_rope_init.argtypes = [_RPP, _I, _I, _I, _I, _D, _I, _D, _D, _D, _D, _D]
+_lib.hisa_rope.argtypes = [_RPP, _P, _P, _P, _I, _I, _I, _P]
+_lib.hisa_cache_store.argtypes = [_AKVP, _P, _P, _P, _P, _I, _P]
+_lib.hisa_cache_load.argtypes = [_AKVP, _P, _P, _P, _P, _I, _P]
+_lib.hisa_block_attn_workspace_bytes.argtypes = [_AKVP, _I, _I, _I, _I]
+_lib.hisa_block_attn_workspace_bytes.restype = _Z
+_lib.hisa_block_attn.argtypes = [_AKVP, _P, _I, _P, _P, _I, _P, _I, _I, _F, _P, _P, _P, _Z, _P]
 _lib.dsa_flat_workspace_bytes.argtypes = [_KVP, _I, _I, _I]
 _lib.dsa_flat_workspace_bytes.restype = _Z
 _lib.dsa_flat_select.argtypes = [_KVP, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]
@@ -111,7 +144,9 @@ for _f in ("hisa_pool_blocks", "hisa_append", "hisa_select", "hisa_decode_step",
            "hisa_select_static",
            "hisa_tree_select", "hisa_pool_tail", "hisa_levels_select", "hisa_cp_blocks", "hisa_cp_tokens",
            "hisa_merge_topk",
-           "hisa_sparse_attn", "dsa_flat_select", "hisa_topk_f32", "hisa_profile_enable", "hisa_profile_read"):
+           "hisa_sparse_attn", "dsa_flat_select", "hisa_topk_f32", "hisa_profile_enable", "hisa_profile_read",
+           "hisa_select_blocks", "hisa_rope_init", "hisa_rope", "hisa_cache_store", "hisa_cache_load",
+           "hisa_block_attn"):
     getattr(_lib, _f).restype = _I
 
 
@@ -606,6 +641,250 @@ def hisa_sparse_attn(Qa: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: t
     _check("hisa_sparse_attn", _lib.hisa_sparse_attn(
         _ptr(Qa), Ha, _ptr(K), _ptr(V), _ptr(lens), batch, cap, d, _ptr(q_seq), _ptr(idx), n_q, k,
         scale, _ptr(out), _ptr(lse), _ptr(status), _ptr(ws), ws.numel(), _stream(stream)))
+    return out, lse
+
+
+class _on:
+    """The device of a call's tensors current, and `stream` (default: that
+    device's current stream) the one that buffers made by the call belong to."""
+
+    def __init__(self, device, stream=None):
+        self.device, self.given = device, stream
+
+    def __enter__(self):
+        self._dev = torch.cuda.device(self.device)
+        self._dev.__enter__()
+        self._str = torch.cuda.stream(self.given if self.given is not None else torch.cuda.current_stream())
+        self._str.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        self._str.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+
+def _want(fn: str, name: str, t, dtype, device, shape):
+    """The library sees pointers only: a tensor of another type, device, shape
+    or layout than the call reads is refused here.  -1 in shape: any size."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.device != device or \
+            t.dim() != len(shape) or any(w >= 0 and n != w for n, w in zip(t.shape, shape)):
+        dims = ", ".join("*" if w < 0 else str(w) for w in shape)
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor [{dims}] on {device}")
+    return t
+
+
+def _want_ws(fn: str, ws: torch.Tensor, device):
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise ValueError(f"{fn}: ws must be a contiguous uint8 tensor on {device}")
+    return ws
+
+
+def hisa_select_blocks_workspace_bytes(kv: KVCache, n_q: int, H: int, m: int) -> int:
+    return int(_lib.hisa_select_blocks_workspace_bytes(kv.struct, n_q, H, m))
+
+
+def hisa_select_blocks(kv: KVCache, Q, w, q_seq, q_pos, m: int, want_counts: bool = False,
+                       ws: Optional[torch.Tensor] = None, blocks: Optional[torch.Tensor] = None, stream=None):
+    """Stage 1 of hisa_select alone: the blocks each row keeps, [n_q, min(m,
+    nblk)] int32 ascending, -1 padded (and with want_counts how many, [n_q])."""
+    fn, dev = "hisa_select_blocks", kv.keys.device
+    with _on(dev, stream) as s:
+        Q, w, q_seq, q_pos = _queries(kv, Q, w, q_seq, q_pos)
+        n_q, H = Q.shape[0], Q.shape[1]
+        _want(fn, "Q", Q, torch.bfloat16, dev, (-1, -1, kv.d))
+        _want(fn, "w", w, torch.float32, dev, (n_q, H))
+        _want(fn, "q_seq", q_seq, torch.int32, dev, (n_q,))
+        if q_pos is not None:
+            _want(fn, "q_pos", q_pos, torch.int32, dev, (n_q,))
+        if ws is None:
+            ws = workspace(hisa_select_blocks_workspace_bytes(kv, n_q, H, m), dev)
+        _want_ws(fn, ws, dev)
+        mm = max(0, min(m, kv.nblk))
+        if blocks is None:
+            blocks = torch.empty((n_q, mm), dtype=torch.int32, device=dev)
+        _want(fn, "blocks", blocks, torch.int32, dev, (n_q, mm))
+        counts = torch.empty(n_q, dtype=torch.int32, device=dev) if want_counts else None
+        _check(fn, _lib.hisa_select_blocks(kv.struct, _ptr(Q), _ptr(w), _ptr(q_seq), _ptr(q_pos), n_q, H, m,
+                                           _ptr(blocks), _ptr(counts), _ptr(ws), ws.numel(), s))
+    return (blocks, counts) if want_counts else blocks
+
+
+def hisa_rope_init(d: int, rot: Optional[int] = None, off: int = 0, layout: str = "half", base: float = 10000.0,
+                   scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0, gain: float = 0.0) -> hisa_rope_plan:
+    """The plan of a rotary embedding: `rot` elements from `off` of rows of d
+    (rot None: all from off on), layout "half" or "interleaved", scaling "none",
+    "linear", "ntk" or "yarn" by `factor`.  Host memory; keep it."""
+    fn = "hisa_rope_init"
+    if layout not in HISA_ROPE_LAYOUTS or scaling not in HISA_ROPE_SCALINGS:
+        raise ValueError(f"{fn}: layout is one of {tuple(HISA_ROPE_LAYOUTS)}, scaling one of {tuple(HISA_ROPE_SCALINGS)}")
+    plan = hisa_rope_plan()
+    _check(fn, _lib.hisa_rope_init(ctypes.byref(plan), d, d - off if rot is None else rot, off,
+                                   HISA_ROPE_LAYOUTS[layout], base, HISA_ROPE_SCALINGS[scaling], factor, orig_len,
+                                   beta_fast, beta_slow, gain))
+    return plan
+
+
+def hisa_rope(plan: hisa_rope_plan, x: torch.Tensor, pos: torch.Tensor, out: Optional[torch.Tensor] = None,
+              transpose: bool = False, stream=None) -> torch.Tensor:
+    """x [rows, heads, d] (or [rows, d]) bf16 rotated by the positions pos
+    [rows] int32; out may be x.  transpose: the map's transpose, which takes
+    the gradient of the result to the gradient of x."""
+    fn = "hisa_rope"
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x must be a CUDA tensor [rows, heads, d] or [rows, d]")
+    rows, heads = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
+    _want(fn, "x", x, torch.bfloat16, x.device, (*x.shape[:-1], plan.d))
+    _want(fn, "pos", pos, torch.int32, x.device, (rows,))
+    with _on(x.device, stream) as s:
+        out = torch.empty_like(x) if out is None else out
+        _want(fn, "out", out, torch.bfloat16, x.device, tuple(x.shape))
+        if out.data_ptr() != x.data_ptr() and x.numel() and \
+                abs(out.data_ptr() - x.data_ptr()) < x.numel() * x.element_size():
+            raise ValueError(f"{fn}: out overlaps x without being x")
+        _check(fn, _lib.hisa_rope(ctypes.byref(plan), _ptr(x), _ptr(out), _ptr(pos), rows, heads, int(transpose), s))
+    return out
+
+
+class AttnCache:
+    """Key and value rows of the attention (hisa_attn_kv): dtype "bf16", or
+    "fp4" (two e2m1 codes to a byte, one e4m3 scale per 16 elements, the value
+    is mul * scale * code).  lens and status: pass the indexer cache's
+    (kv.len, kv.status) to share them."""
+
+    def __init__(self, batch: int, cap: int, heads: int, d: int, dtype: str = "bf16", lens: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, k_mul: float = 1.0, v_mul: float = 1.0, device="cuda"):
+        if dtype not in ("bf16", "fp4"):
+            raise ValueError("AttnCache: dtype must be 'bf16' or 'fp4'")
+        dev = lens.device if lens is not None else torch.device(device)
+        shape = (batch, heads, cap)
+        zeros = lambda n, dt: torch.zeros((*shape, n), dtype=dt, device=dev)  # noqa: E731
+        if dtype == "bf16":
+            k, v, ks, vs = zeros(d, torch.bfloat16), zeros(d, torch.bfloat16), None, None
+        else:
+            k, v = zeros(d // 2, torch.uint8), zeros(d // 2, torch.uint8)
+            ks, vs = zeros(d // 16, torch.uint8), zeros(d // 16, torch.uint8)
+        if lens is None:
+            lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self._take(k, v, lens, ks, vs, status, k_mul, v_mul)
+
+    @classmethod
+    def wrap(cls, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+             v_scale: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, k_mul: float = 1.0,
+             v_mul: float = 1.0) -> "AttnCache":
+        """A cache over tensors the caller has: k, v [batch, heads, cap, d] bf16,
+        or [.., d / 2] uint8 with k_scale, v_scale [.., d / 16] (uint8 or e4m3)."""
+        c = cls.__new__(cls)
+        c._take(k, v, lens, k_scale, v_scale, status, k_mul, v_mul)
+        return c
+
+    def _take(self, k, v, lens, ks, vs, status, k_mul, v_mul):
+        fn = "AttnCache"
+        if (ks is None) != (vs is None):
+            raise ValueError(f"{fn}: k_scale and v_scale come together")
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError(f"{fn}: k must be a tensor [batch, heads, cap, d or d / 2]")
+        fp4, dev = ks is not None, k.device
+        self.batch, self.heads, self.cap = (int(n) for n in k.shape[:3])
+        self.d = int(k.shape[3]) * (2 if fp4 else 1)
+        dt = torch.uint8 if fp4 else torch.bfloat16
+        _want(fn, "k", k, dt, dev, tuple(k.shape))
+        _want(fn, "v", v, dt, dev, tuple(k.shape))
+        if fp4:
+            ks, vs = (x.view(torch.uint8) if isinstance(x, torch.Tensor) and x.dtype == torch.float8_e4m3fn else x
+                      for x in (ks, vs))
+            for name, x in (("k_scale", ks), ("v_scale", vs)):
+                _want(fn, name, x, torch.uint8, dev, (*k.shape[:3], self.d // 16))
+        _want(fn, "lens", lens, torch.int32, dev, (self.batch,))
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=dev)
+        _want(fn, "status", status, torch.int32, dev, (1,))
+        self.k, self.v, self.k_scale, self.v_scale, self.len, self.status = k, v, ks, vs, lens, status
+        self.dtype, self.device, self.k_mul, self.v_mul = "fp4" if fp4 else "bf16", dev, float(k_mul), float(v_mul)
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self._struct = hisa_attn_kv(
+            k=ptr(k), v=ptr(v), k_scale=ptr(ks), v_scale=ptr(vs), len=ptr(lens), status=ptr(status), batch=self.batch,
+            cap=self.cap, heads=self.heads, d=self.d, dtype=HISA_CACHE_FP4 if fp4 else HISA_CACHE_BF16,
+            k_mul=self.k_mul, v_mul=self.v_mul)
+
+    @property
+    def struct(self):
+        return ctypes.byref(self._struct)
+
+    def status_bits(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF
+
+    def clear_status(self):
+        self.status.zero_()
+
+
+def _cache_names(fn, c, seq, pos):
+    _want(fn, "seq", seq, torch.int32, c.device, (-1,))
+    if pos is not None:
+        _want(fn, "pos", pos, torch.int32, c.device, (seq.shape[0],))
+    return seq.shape[0]
+
+
+def hisa_cache_store(c: AttnCache, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor,
+                     pos: Optional[torch.Tensor] = None, stream=None):
+    """Tokens' key and value rows K, V [n, heads, d] bf16 into the cache at
+    (seq[i], pos[i]); pos None: each sequence's last position len - 1."""
+    fn = "hisa_cache_store"
+    n = _cache_names(fn, c, seq, pos)
+    for name, t in (("K", K), ("V", V)):
+        _want(fn, name, t, torch.bfloat16, c.device, (n, c.heads, c.d))
+    with _on(c.device, stream) as s:
+        _check(fn, _lib.hisa_cache_store(c.struct, _ptr(K), _ptr(V), _ptr(seq), _ptr(pos), n, s))
+
+
+def hisa_cache_load(c: AttnCache, seq: torch.Tensor, pos: Optional[torch.Tensor] = None,
+                    K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
+    """The values (K, V) [n, heads, d] bf16 that the rows at (seq[i], pos[i]) stand for."""
+    fn = "hisa_cache_load"
+    n = _cache_names(fn, c, seq, pos)
+    with _on(c.device, stream) as s:
+        K = torch.empty((n, c.heads, c.d), dtype=torch.bfloat16, device=c.device) if K is None else K
+        V = torch.empty((n, c.heads, c.d), dtype=torch.bfloat16, device=c.device) if V is None else V
+        for name, t in (("K", K), ("V", V)):
+            _want(fn, name, t, torch.bfloat16, c.device, (n, c.heads, c.d))
+        _check(fn, _lib.hisa_cache_load(c.struct, _ptr(K), _ptr(V), _ptr(seq), _ptr(pos), n, s))
+    return K, V
+
+
+def hisa_block_attn_workspace_bytes(c: AttnCache, n_q: int, Hq: int, B: int, mb: int) -> int:
+    """mb: kept blocks per row (the width of `blocks`), 0 for the whole prefix."""
+    return int(_lib.hisa_block_attn_workspace_bytes(c.struct, n_q, Hq, B, mb))
+
+
+def hisa_block_attn(c: AttnCache, Qa: torch.Tensor, q_seq: torch.Tensor, q_pos: Optional[torch.Tensor] = None,
+                    blocks: Optional[torch.Tensor] = None, B: int = 128, scale: Optional[float] = None,
+                    ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of query rows Qa [n_q, Hq, d] bf16 over the tokens of their kept
+    blocks [n_q, mb] of B tokens (blocks None: the whole prefix), up to each
+    row's position.  Returns (out [n_q, Hq, d] bf16, lse [n_q, Hq] fp32)."""
+    fn, dev = "hisa_block_attn", c.device
+    _want(fn, "Qa", Qa, torch.bfloat16, dev, (-1, -1, c.d))
+    n_q, Hq = Qa.shape[0], Qa.shape[1]
+    _want(fn, "q_seq", q_seq, torch.int32, dev, (n_q,))
+    if q_pos is not None:
+        _want(fn, "q_pos", q_pos, torch.int32, dev, (n_q,))
+    if blocks is not None:
+        _want(fn, "blocks", blocks, torch.int32, dev, (n_q, -1))
+        if blocks.shape[1] < 1:
+            raise ValueError(f"{fn}: blocks must have a column (None: the whole prefix)")
+    mb = 0 if blocks is None else blocks.shape[1]
+    scale = (1.0 / c.d ** 0.5) if scale is None else float(scale)
+    with _on(dev, stream) as s:
+        if ws is None:
+            ws = workspace(hisa_block_attn_workspace_bytes(c, n_q, Hq, B, mb), dev)
+        _want_ws(fn, ws, dev)
+        out = torch.empty((n_q, Hq, c.d), dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty((n_q, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        _want(fn, "out", out, torch.bfloat16, dev, (n_q, Hq, c.d))
+        _want(fn, "lse", lse, torch.float32, dev, (n_q, Hq))
+        _check(fn, _lib.hisa_block_attn(c.struct, _ptr(Qa), Hq, _ptr(q_seq), _ptr(q_pos), n_q, _ptr(blocks), mb, B,
+                                        scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s))
     return out, lse
 
 

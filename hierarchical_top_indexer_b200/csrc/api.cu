@@ -261,6 +261,21 @@ HisaWs hisa_ws(const KvView& v, int n_q, int H, int m) {
     return w;
 }
 
+// Stage 1 alone (hisa_select_blocks).
+HisaWs blocks_ws(const KvView& v, int n_q, int m) {
+    HisaWs w;
+    std::memset(&w, 0, sizeof w);
+    w.mm = m < v.nblk ? m : v.nblk;
+    w.ldb = static_cast<int>(round_up(v.nblk, 128));
+    Carve c;
+    w.bkeys = c.take(static_cast<size_t>(n_q) * w.ldb * 4);
+    w.blocks = c.take(static_cast<size_t>(n_q) * w.mm * 4);
+    w.nblocks = c.take(static_cast<size_t>(n_q) * 4);
+    w.plan = c.take(static_cast<size_t>(n_q) * 16);
+    w.total = c.off;
+    return w;
+}
+
 size_t flat_ld(const KvView& v) { return round_up(v.cap, 128); }
 
 // The CUDA error behind the calling thread's last HISA_E_CUDA.
@@ -753,6 +768,106 @@ bool gathered_level(int bf, int W, int nblk, int n_q) {
            4 * children <= nblk && n_q <= 2 * sm_count();
 }
 
+// ---------------------------------------------------- the attention's cache
+
+bool power_of_two(float x) {
+    int e;
+    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e >= -59 && e <= 61;
+}
+
+int check_attn_kv(const hisa_attn_kv* c) {
+    if (!c || !c->k || !c->v || !c->len) return HISA_E_INVAL;
+    if (c->batch < 1 || c->cap < 1 || c->heads < 1) return HISA_E_INVAL;
+    if (c->dtype != HISA_CACHE_BF16 && c->dtype != HISA_CACHE_FP4) return HISA_E_INVAL;
+    if (c->d != 64 && c->d != 128) return HISA_E_UNSUPPORTED;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->len, 4) || (c->status && !aligned(c->status, 4)))
+        return HISA_E_INVAL;
+    // list entries hold a sequence in 23 bits; a head's rows are counted in 31
+    if (c->batch >= 1 << 23 || static_cast<long long>(c->batch) * c->heads > INT_MAX ||
+        static_cast<long long>(c->batch) * c->heads * c->cap > (1ll << 40))
+        return HISA_E_UNSUPPORTED;
+    if (c->dtype == HISA_CACHE_FP4) {
+        if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return HISA_E_INVAL;
+        if (!power_of_two(c->k_mul) || !power_of_two(c->v_mul)) return HISA_E_INVAL;
+        if (c->cap % 16 != 0) return HISA_E_UNSUPPORTED;
+    }
+    return HISA_OK;
+}
+
+// The cache's rows [n, heads, d] named by (seq, pos).
+int check_cache_rows(const hisa_attn_kv* c, const void* K, const void* V, const int32_t* seq, const int32_t* pos, int n) {
+    const int rc = check_attn_kv(c);
+    if (rc) return rc;
+    if (n < 0) return HISA_E_INVAL;
+    if (n == 0) return HISA_OK;
+    if (!K || !V || !seq || !aligned(K, 16) || !aligned(V, 16) || !aligned(seq, 4) || (pos && !aligned(pos, 4)))
+        return HISA_E_INVAL;
+    if (static_cast<long long>(n) * c->heads * (c->d / 16) > INT_MAX * 256ll) return HISA_E_UNSUPPORTED;
+    return HISA_OK;
+}
+
+CacheParams cache_params(const hisa_attn_kv* c, const int32_t* seq, const int32_t* pos, int n) {
+    CacheParams p;
+    std::memset(&p, 0, sizeof p);
+    p.k = c->k;
+    p.v = c->v;
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.len = c->len;
+    p.status = c->status;
+    p.batch = c->batch;
+    p.cap = c->cap;
+    p.heads = c->heads;
+    p.d = c->d;
+    p.n = n;
+    p.fp4 = c->dtype == HISA_CACHE_FP4;
+    p.k_mul = c->k_mul;
+    p.v_mul = c->v_mul;
+    p.seq = seq;
+    p.pos = pos;
+    return p;
+}
+
+// Sizes of a block-attention call on a checked cache (workspace layout at ws).
+int battn_params(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb, void* ws, BattnParams* p, size_t* bytes) {
+    if (n_q < 0 || Hq < 1 || mb < 0) return HISA_E_INVAL;
+    if (Hq % c->heads != 0) return HISA_E_INVAL;
+    if (Hq / c->heads > 128) return HISA_E_UNSUPPORTED;
+    if (mb > 0 && (!select_block_size_ok(B) || (static_cast<long long>(c->cap) + B - 1) / B > 1 << 20)) return HISA_E_UNSUPPORTED;
+    std::memset(p, 0, sizeof *p);
+    p->len = c->len;
+    p->status = c->status;
+    p->batch = c->batch;
+    p->cap = c->cap;
+    p->Hkv = c->heads;
+    p->Hq = Hq;
+    p->d = c->d;
+    p->n_q = n_q;
+    p->B = B;
+    p->mb = mb;
+    *bytes = battn_layout(*p, ws);
+    // tile numbers and grids are 32-bit
+    const long long tiles = (static_cast<long long>(p->lcap) / p->S + 1) * p->groups;
+    if (p->lcap < 0 || tiles > INT_MAX || static_cast<long long>(p->groups) * p->Hkv > INT_MAX ||
+        static_cast<long long>(p->R) * mb > INT_MAX)
+        return HISA_E_UNSUPPORTED;
+    return HISA_OK;
+}
+
+// [rows, heads, d] bf16 as a 3-D tensor with boxes of [box_rows, box_heads, 64].
+bool heads_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, int d, uint32_t box_rows,
+               uint32_t box_heads) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), heads, rows};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, heads * d * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1187,6 +1302,191 @@ int hisa_sparse_attn(const uint16_t* Qa, int Ha, const uint16_t* Kc, const uint1
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     PhaseScope ps(HISA_PHASE_ATTN, s);
     return cuda_status(launch_attn(p, sms, s));
+}
+
+size_t hisa_select_blocks_workspace_bytes(const hisa_kv* kv, int n_q, int H, int m) {
+    KvView v;
+    if (check_kv(kv, &v) || n_q < 0 || H < 1 || H > 128 || m < 1) return 0;
+    return blocks_ws(v, n_q, m).total;
+}
+
+int hisa_select_blocks(const hisa_kv* kv, const uint16_t* Q, const float* w, const int32_t* q_seq, const int32_t* q_pos,
+                       int n_q, int H, int m, int32_t* blocks, int32_t* nblocks, void* ws, size_t ws_bytes,
+                       hisa_stream_t stream) {
+    KvView v;
+    int rc = check_kv(kv, &v);
+    if (rc) return rc;
+    if (!select_block_size_ok(v.B)) return HISA_E_UNSUPPORTED;
+    if (m < 1) return HISA_E_INVAL;
+    rc = check_queries(Q, w, q_seq, n_q, H, 1, blocks);
+    if (rc) return rc;
+    if (n_q == 0) return HISA_OK;
+    if ((q_pos && !aligned(q_pos, 4)) || (nblocks && !aligned(nblocks, 4))) return HISA_E_INVAL;
+    const HisaWs L = blocks_ws(v, n_q, m);
+    if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return HISA_E_WORKSPACE;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    BlockLevel lv;
+    std::memset(&lv, 0, sizeof lv);
+    lv.v = &v;
+    lv.m = m;
+    lv.mm = L.mm;
+    lv.ldb = L.ldb;
+    lv.bkeys = reinterpret_cast<uint32_t*>(base + L.bkeys);
+    lv.blocks = reinterpret_cast<int32_t*>(base + L.blocks);
+    lv.nblocks = reinterpret_cast<int32_t*>(base + L.nblocks);
+    lv.plan = reinterpret_cast<int4*>(base + L.plan);
+    lv.blocks_out = blocks;
+    lv.nblocks_out = nblocks;
+    return block_stage(lv, Q, w, q_seq, q_pos, n_q, H, 1, nullptr, 2, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, double base, int scaling, double factor,
+                   double orig_len, double beta_fast, double beta_slow, double gain) {
+    if (!plan) return HISA_E_INVAL;
+    std::memset(plan, 0, sizeof *plan);
+    if (d < 2 || d > 512 || rot < 2 || rot % 2 != 0 || rot > 2 * HISA_ROPE_MAX_PAIRS || off < 0 || off > d - rot)
+        return HISA_E_INVAL;
+    if (layout != HISA_ROPE_HALF && layout != HISA_ROPE_INTERLEAVED) return HISA_E_INVAL;
+    if (scaling < HISA_ROPE_NONE || scaling > HISA_ROPE_YARN) return HISA_E_INVAL;
+    if (!std::isfinite(base) || !(base > 1.0) || !std::isfinite(factor) || !(factor >= 1.0) || !std::isfinite(gain))
+        return HISA_E_INVAL;
+    if (scaling == HISA_ROPE_NTK && rot == 2) return HISA_E_INVAL;
+    const long double two_pi = 6.283185307179586476925286766559L;
+    long double b = base, lo = 0, hi = 0;
+    if (scaling == HISA_ROPE_NTK) b *= powl(factor, static_cast<long double>(rot) / (rot - 2));
+    if (scaling == HISA_ROPE_YARN) {
+        if (!std::isfinite(orig_len) || !(orig_len > 0) || !std::isfinite(beta_fast) || !(beta_slow > 0) ||
+            !(beta_fast >= beta_slow))
+            return HISA_E_INVAL;
+        const auto at = [&](double turns) { return rot * logl(orig_len / (turns * two_pi)) / (2 * logl(base)); };
+        lo = floorl(at(beta_fast));
+        hi = ceill(at(beta_slow));
+        lo = lo > 0 ? lo : 0;
+        hi = hi < rot - 1 ? hi : rot - 1;
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        long double w = powl(b, -2.0L * i / rot);
+        if (scaling == HISA_ROPE_LINEAR) w /= factor;
+        if (scaling == HISA_ROPE_YARN) {
+            const long double span = hi - lo > 0.001L ? hi - lo : 0.001L;
+            long double r = (i - lo) / span;
+            r = r < 0 ? 0 : r > 1 ? 1 : r;
+            w = w * (1 - r) + w / factor * r;
+        }
+        const long double t = w / two_pi;   // in (0, 0.16]
+        plan->turns[i] = static_cast<uint64_t>(rintl(ldexpl(t, 64)));
+    }
+    plan->d = d;
+    plan->rot = rot;
+    plan->off = off;
+    plan->layout = layout;
+    plan->gain = static_cast<float>(gain != 0.0 ? gain : scaling == HISA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0);
+    plan->ready = 1;
+    return HISA_OK;
+}
+
+int hisa_rope(const hisa_rope_plan* plan, const uint16_t* x, uint16_t* y, const int32_t* pos, int rows, int heads,
+              int transpose, hisa_stream_t stream) {
+    if (!plan || plan->ready != 1 || rows < 0 || heads < 1 || heads > 1 << 16) return HISA_E_INVAL;
+    if (plan->rot < 2 || plan->rot > 2 * HISA_ROPE_MAX_PAIRS || plan->d < plan->rot || plan->d > 512 || plan->off < 0 ||
+        plan->off > plan->d - plan->rot)
+        return HISA_E_INVAL;
+    if (rows == 0) return HISA_OK;
+    if (!x || !y || !pos || !aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return HISA_E_INVAL;
+    const int sms = sm_count();
+    if (sms <= 0) return HISA_E_CUDA;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x;
+    p.y = y;
+    p.pos = pos;
+    p.rows = rows;
+    p.heads = heads;
+    p.d = plan->d;
+    p.rot = plan->rot;
+    p.off = plan->off;
+    p.interleaved = plan->layout == HISA_ROPE_INTERLEAVED;
+    p.transpose = transpose != 0;
+    p.gain = plan->gain;
+    std::memcpy(p.turns, plan->turns, sizeof p.turns);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    PhaseScope ps(HISA_PHASE_ROPE, s);
+    return cuda_status(launch_rope(p, sms, s));
+}
+
+int hisa_cache_store(const hisa_attn_kv* c, const uint16_t* K, const uint16_t* V, const int32_t* seq, const int32_t* pos,
+                     int n, hisa_stream_t stream) {
+    const int rc = check_cache_rows(c, K, V, seq, pos, n);
+    if (rc || n == 0) return rc;
+    CacheParams p = cache_params(c, seq, pos, n);
+    p.k_rows = K;
+    p.v_rows = V;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    PhaseScope ps(HISA_PHASE_CACHE, s);
+    return cuda_status(launch_cache_store(p, s));
+}
+
+int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32_t* seq, const int32_t* pos, int n,
+                    hisa_stream_t stream) {
+    const int rc = check_cache_rows(c, K, V, seq, pos, n);
+    if (rc || n == 0) return rc;
+    CacheParams p = cache_params(c, seq, pos, n);
+    p.k_out = K;
+    p.v_out = V;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    PhaseScope ps(HISA_PHASE_CACHE, s);
+    return cuda_status(launch_cache_load(p, s));
+}
+
+size_t hisa_block_attn_workspace_bytes(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb) {
+    BattnParams p;
+    size_t bytes = 0;
+    if (check_attn_kv(c) || battn_params(c, n_q, Hq, B, mb, nullptr, &p, &bytes)) return 0;
+    return bytes;
+}
+
+int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int32_t* q_seq, const int32_t* q_pos, int n_q,
+                    const int32_t* blocks, int mb, int B, float scale, uint16_t* out, float* lse, void* ws,
+                    size_t ws_bytes, hisa_stream_t stream) {
+    int rc = check_attn_kv(c);
+    if (rc) return rc;
+    BattnParams p;
+    size_t need = 0;
+    rc = battn_params(c, n_q, Hq, B, mb, ws, &p, &need);
+    if (rc) return rc;
+    if (!(scale > 0.f) || !std::isfinite(scale) || (mb > 0) != (blocks != nullptr)) return HISA_E_INVAL;
+    if (n_q == 0) return HISA_OK;
+    if (!Qa || !q_seq || !out || !aligned(Qa, 16) || !aligned(out, 16) || !aligned(q_seq, 4) ||
+        (q_pos && !aligned(q_pos, 4)) || (blocks && !aligned(blocks, 4)) || (lse && !aligned(lse, 4)))
+        return HISA_E_INVAL;
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return HISA_E_WORKSPACE;
+    const bool fp4 = c->dtype == HISA_CACHE_FP4;
+    p.q = Qa;
+    p.q_seq = q_seq;
+    p.q_pos = q_pos;
+    p.blocks = blocks;
+    p.k4 = static_cast<const uint8_t*>(c->k);
+    p.v4 = static_cast<const uint8_t*>(c->v);
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.scale_log2 = scale * 1.4426950408889634f * (fp4 ? c->k_mul : 1.f);
+    p.out_mul = fp4 ? c->v_mul : 1.f;
+    p.out = out;
+    p.lse = lse;
+    const int sms = sm_count();
+    if (sms <= 0) return HISA_E_CUDA;
+    CUtensorMap qm, km, vm;
+    std::memset(&qm, 0, sizeof qm);
+    km = vm = qm;
+    if (!fp4) {
+        const uint64_t bh = static_cast<uint64_t>(c->batch) * c->heads;
+        if (!heads_map(&qm, Qa, n_q, Hq, c->d, p.R, p.G) || !heads_map(&km, c->k, bh, c->cap, c->d, 1, p.PB) ||
+            !heads_map(&vm, c->v, bh, c->cap, c->d, 1, p.PB))
+            return HISA_E_CUDA;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    PhaseScope ps(HISA_PHASE_BLOCK_ATTN, s);
+    return cuda_status(launch_battn(qm, km, vm, p, fp4, sms, s));
 }
 
 int hisa_selftest_wait(uint32_t* status, hisa_stream_t stream) {

@@ -47,57 +47,15 @@ struct AttnLayout {
     static constexpr int lred = red + 2048;        // [2][128] fp32 sums of the halves
 };
 
-// Byte offset of 16-byte chunk c (0..15) of row r (0..127) of a 128 x 128
-// bf16 operand in the 128-byte swizzled layout: two 64-column atoms of 16 KB,
-// rows of 128 B, chunk index XOR (row mod 8).
-__device__ __forceinline__ uint32_t sw128_off(int r, int c) {
-    return static_cast<uint32_t>((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // 16-byte asynchronous copy global -> shared; src_bytes = 0 writes zeros.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                  : "memory");
 }
 
-// 32 lanes x 32 bit, 16 consecutive columns per thread (TMEM store).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Descriptor of an MN-major operand in the 128-byte swizzled layout: atoms of
-// 64 MN-elements x 8 K-rows (1 KB); the two 64-wide MN atoms are 16 KB apart
-// (leading offset), consecutive 8-row K groups 1 KB apart (stride offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(16384 >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-
 // bf16 x bf16 -> fp32, M = N = 128, A K-major; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_attn(bool b_mn_major) {
     return idesc_bf16_f32(128) | (b_mn_major ? (1u << 16) : 0u);
-}
-
-// 2^x by the hardware approximation (about 2^-22 relative; 2^-inf = 0).
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 struct Seg {

@@ -215,6 +215,74 @@ size_t attn_workspace_bytes(int n_q, int k);
 void attn_carve(AttnParams& p, void* ws);
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t s);
 
+// Rotary positions (rope.cu).
+struct RopeParams {
+    const uint16_t* x;       // [rows, heads, d] bf16
+    uint16_t* y;             // the same shape; may be x
+    const int32_t* pos;      // [rows]
+    int rows, heads, d, rot, off;
+    int interleaved, transpose;
+    float gain;
+    int tasks, rows_blk, heads_blk;      // set by launch_rope
+    uint64_t turns[HISA_ROPE_MAX_PAIRS]; // turns per position of each pair, 64-bit fixed point
+};
+cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s);
+
+// Rows of the attention cache stored and read back (cache.cu).
+struct CacheParams {
+    void* k;                 // [batch, heads, cap, d] bf16, or [.., d / 2] e2m1 codes
+    void* v;
+    uint8_t* k_scale;        // [batch, heads, cap, d / 16] e4m3 (4-bit rows)
+    uint8_t* v_scale;
+    const int32_t* len;
+    uint32_t* status;
+    int batch, cap, heads, d, n;
+    bool fp4;
+    float k_mul, v_mul;
+    const int32_t* seq;      // [n]
+    const int32_t* pos;      // [n], or null: len[seq] - 1
+    const uint16_t* k_rows;  // store: [n, heads, d] bf16
+    const uint16_t* v_rows;
+    uint16_t* k_out;         // load: the same shape
+    uint16_t* v_out;
+};
+cudaError_t launch_cache_store(const CacheParams& p, cudaStream_t s);
+cudaError_t launch_cache_load(const CacheParams& p, cudaStream_t s);
+
+// Block-sparse attention (battn.cu).
+constexpr int kBattnMaxGrid = 148;   // CTAs (one per SM) whose partial outputs the workspace holds
+struct BattnParams {
+    const uint16_t* q;       // [n_q, Hq, d] bf16
+    const int32_t* q_seq;    // [n_q]
+    const int32_t* q_pos;    // [n_q] or null: len[q_seq] - 1
+    const int32_t* blocks;   // [n_q, mb] kept blocks, or null: the whole prefix
+    const int32_t* len;
+    uint32_t* status;
+    const uint8_t* k4;       // 4-bit rows (bf16 rows come by tensor map)
+    const uint8_t* v4;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    int batch, cap, Hkv, Hq, d, n_q, B, mb;
+    float scale_log2;        // softmax scale * log2(e) * k_mul
+    float out_mul;           // v_mul
+    uint16_t* out;           // [n_q, Hq, d] bf16
+    float* lse;              // [n_q, Hq] or null
+    // set by battn_layout
+    int G, R, groups;        // heads per key head, rows per group, groups
+    int PB, S, ppb;          // tokens per piece, pieces per tile, pieces per block
+    int W, lcap;             // words of a row's block bitmap, pieces a group's list holds
+    int2* list;              // workspace: [groups, lcap]
+    int* pieces;             // [groups]
+    int* tile0;              // [groups + 1] tiles of the groups before
+    uint32_t* bits;          // [n_q, W] (R > 1)
+    float* part_o;           // [2 * grid, 128, d]
+    float2* part_ml;         // [2 * grid, 128] maximum (log2 domain) and sum
+};
+// Fills in the derived sizes and the workspace pointers; returns the bytes.
+size_t battn_layout(BattnParams& p, void* ws);
+cudaError_t launch_battn(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                         const BattnParams& p, bool fp4, int sms, cudaStream_t s);
+
 // One warp waiting on an mbarrier that never completes (diag.cu).
 cudaError_t launch_wait_probe(uint32_t* status, cudaStream_t s);
 

@@ -395,6 +395,164 @@ int hisa_sparse_attn(const uint16_t* Qa, int Ha, const uint16_t* Kc, const uint1
                      hisa_stream_t stream);
 
 /*
+ * hisa_select_blocks — stage 1 of hisa_select alone: the blocks each row
+ * keeps (HISA arXiv abstract, stage (1); gptget.net summary, "Methodology"),
+ * for a consumer that attends to whole blocks (hisa_block_attn).
+ *   blocks  [n_q, min(m, nblk)] int32 out: kept block ids per row, ascending,
+ *           -1 padded: the own block and the best m - 1 others, exactly the
+ *           blocks hisa_select_inspect reports
+ *   nblocks [n_q] int32 out (or NULL): how many
+ * The other arguments and errors as hisa_select.  A row whose position is not
+ * inside its prefix gets -1 entries and sets HISA_DEV_BAD_QUERY.
+ */
+size_t hisa_select_blocks_workspace_bytes(const hisa_kv* kv, int n_q, int H, int m);
+int hisa_select_blocks(const hisa_kv* kv, const uint16_t* Q, const float* w, const int32_t* q_seq,
+                       const int32_t* q_pos, int n_q, int H, int m, int32_t* blocks, int32_t* nblocks,
+                       void* ws, size_t ws_bytes, hisa_stream_t stream);
+
+/*
+ * Rotary positions (no counterpart on the pages, whose queries and keys come
+ * with their positions in them): hisa_rope_init fills a plan (host memory),
+ * hisa_rope applies it to query or key rows before they are scored, appended
+ * or stored.  Pair i of the rotated part, (a, b), becomes at position p
+ *     (g (a cos t - b sin t), g (b cos t + a sin t)),   t = p * w_i
+ *   d        row length, 2..512; rot: rotated elements, even, 2..256, starting
+ *            at element off (off + rot <= d); the others are copied
+ *   layout   HALF: pair i is elements off + i and off + i + rot / 2;
+ *            INTERLEAVED: off + 2i and off + 2i + 1
+ *   scaling  NONE:   w_i = base^(-2i / rot)
+ *            LINEAR: w_i / factor
+ *            NTK:    base * factor^(rot / (rot - 2)) in place of base (rot > 2)
+ *            YARN:   w_i (1 - r_i) + (w_i / factor) r_i with the ramp
+ *                    r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1) between
+ *                    lo = max(floor(c(beta_fast)), 0) and
+ *                    hi = min(ceil(c(beta_slow)), rot - 1), where
+ *                    c(t) = rot ln(orig_len / (2 pi t)) / (2 ln base)
+ *   gain     g; 0: the scaling's own, 0.1 ln(factor) + 1 for YARN, else 1
+ * factor >= 1; base > 1; YARN: orig_len > 0, beta_fast >= beta_slow > 0.
+ * Angles are exact to about 2^-31 of a turn at every 32-bit position,
+ * negative ones included.
+ */
+#define HISA_ROPE_MAX_PAIRS 128
+enum hisa_rope_layout { HISA_ROPE_HALF = 0, HISA_ROPE_INTERLEAVED = 1 };
+enum hisa_rope_scaling {
+    HISA_ROPE_NONE = 0,
+    HISA_ROPE_LINEAR = 1,
+    HISA_ROPE_NTK = 2,
+    HISA_ROPE_YARN = 3
+};
+typedef struct hisa_rope_plan {
+    int32_t d, rot, off, layout;
+    float gain;
+    int32_t ready;   /* set by hisa_rope_init */
+    uint64_t turns[HISA_ROPE_MAX_PAIRS];   /* turns per position, times 2^64 */
+} hisa_rope_plan;
+int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, double base, int scaling,
+                   double factor, double orig_len, double beta_fast, double beta_slow, double gain);
+
+/*
+ * hisa_rope — y = the rotated rows of x.
+ *   x, y   [rows, heads, d] bf16; y may be x (in place) but not overlap it otherwise
+ *   pos    [rows] int32: the position of each row (hisa_kv.len before an
+ *          append names the position of the token about to be appended)
+ *   transpose  0, or 1 for the transposed map (t negated): the gradient of the
+ *          rows from the gradient of the rotated rows
+ * The angle is taken modulo a turn in 64-bit fixed point, the rotation in
+ * fp32, rounded once to bf16.  Errors: HISA_E_INVAL (plan not initialised,
+ * sizes, pointers, alignment), HISA_E_CUDA.
+ */
+int hisa_rope(const hisa_rope_plan* plan, const uint16_t* x, uint16_t* y, const int32_t* pos, int rows,
+              int heads, int transpose, hisa_stream_t stream);
+
+/*
+ * The attention cache: key and value rows of the tokens whose indexer keys
+ * hisa_kv holds, in bf16 or in 4 bits.
+ *   k, v     BF16: [batch, heads, cap, d] bf16
+ *            FP4:  [batch, heads, cap, d / 2] bytes of two e2m1 codes, the
+ *                  element of even index in the low half
+ *   k_scale, v_scale  FP4: [batch, heads, cap, d / 16] e4m3, one per 16
+ *                  elements (NULL for BF16); the value of an element is
+ *                  mul * scale * code, which bf16 holds exactly
+ *   len      [batch] int32 valid tokens per sequence: usually hisa_kv.len
+ *   status   [1] device status word or NULL: usually hisa_kv.status
+ *   heads    key heads; d in {64, 128}; FP4: cap a multiple of 16
+ *   k_mul, v_mul  FP4: the factor of all keys (values), a power of two within
+ *                  2^-60 .. 2^60; 1 suits groups of 16 whose largest element
+ *                  lies between 2^-3 and 2688 (e4m3 scales end at 448 and lose
+ *                  precision below 2^-6); not read for BF16
+ * Rows at positions below len must hold finite values; rows at or past len
+ * may hold anything.
+ */
+enum hisa_cache_dtype { HISA_CACHE_BF16 = 0, HISA_CACHE_FP4 = 1 };
+typedef struct hisa_attn_kv {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int32_t* len;
+    uint32_t* status;
+    int32_t batch, cap, heads, d;
+    int32_t dtype;   /* enum hisa_cache_dtype */
+    float k_mul, v_mul;
+} hisa_attn_kv;
+
+/*
+ * hisa_cache_store — n new tokens' key and value rows into the cache (no
+ * counterpart on the pages; the attention-side twin of hisa_append).
+ *   K, V   [n, heads, d] bf16
+ *   seq    [n] int32 sequence of each token
+ *   pos    [n] int32 position of each token in 0 .. cap - 1; NULL: each
+ *          sequence's last position len[seq] - 1 (a decode step: after
+ *          hisa_append or hisa_decode_step has advanced the shared len)
+ * Reads len only for pos = NULL and never changes it.  FP4 rows are
+ * quantised: per 16 elements scale = e4m3(min(448, max|x| / (6 mul))), code =
+ * e2m1(x / (mul * scale)), both to nearest with ties to even, codes saturated
+ * at 6.  Each (seq, pos) may be named once in a call; which row a position
+ * named twice holds afterwards is undefined (it may mix them).  A token with a
+ * bad sequence (HISA_DEV_BAD_QUERY) or position (HISA_DEV_CAPACITY) is skipped.
+ * hisa_cache_load — the way back: K, V [n, heads, d] bf16 out, the values the
+ * cache's rows stand for; a zero row and a status bit for a bad name.
+ * Errors: HISA_E_INVAL, HISA_E_UNSUPPORTED (d, cap), HISA_E_CUDA.
+ */
+int hisa_cache_store(const hisa_attn_kv* c, const uint16_t* K, const uint16_t* V, const int32_t* seq,
+                     const int32_t* pos, int n, hisa_stream_t stream);
+int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32_t* seq,
+                    const int32_t* pos, int n, hisa_stream_t stream);
+
+/*
+ * hisa_block_attn — attention of each query row over all tokens of its kept
+ * blocks, or over its whole prefix (the coarse form of hisa_sparse_attn: HISA
+ * blog, "How Fine-Grained Sparse Attention Works Today", attention over a
+ * selection; gptget.net summary, "Novelty", block-sparse attention).  Hq query
+ * heads share the cache's key heads in order, G = Hq / heads per key head.  For
+ * row i of sequence b at position t, head h, over the tokens s <= t of its kept
+ * blocks:
+ *     z_s = scale * Qa[i, h] . K[b, h / G, s]
+ *     out[i, h] = sum_s exp(z_s) V[b, h / G, s] / sum_s exp(z_s)
+ *     lse[i, h] = log sum_s exp(z_s)
+ *   Qa     [n_q, Hq, d] bf16; q_seq [n_q], q_pos [n_q] or NULL (the row's last
+ *          position, len - 1)
+ *   blocks [n_q, mb] int32: kept block ids of B tokens, in any order (the
+ *          output of hisa_select_blocks or hisa_select_inspect); entries that
+ *          are negative or lie past the row's position are skipped, a repeated
+ *          id counts once.  NULL with mb = 0: the whole prefix (B is not read)
+ *   out    [n_q, Hq, d] bf16; lse [n_q, Hq] fp32 or NULL
+ *   ws     workspace of at least hisa_block_attn_workspace_bytes(...) bytes
+ * A row that sees no token gives out = 0 and lse = -inf; a row whose position
+ * is not inside its prefix does too, and sets HISA_DEV_BAD_QUERY.  Sizes: B as
+ * hisa_select, at most 2^20 blocks per sequence, G in 1..128.
+ * Numerics: logits from exact products (bf16, or f16 for FP4 rows) summed in
+ * fp32; softmax maxima and sums in fp32; the weights are rounded to bf16 (f16
+ * for FP4 rows) for the product with the values, accumulated in fp32; out is
+ * rounded once to bf16.  Results do not depend on the order of atomics.
+ * Errors: HISA_E_INVAL, HISA_E_UNSUPPORTED, HISA_E_WORKSPACE, HISA_E_CUDA.
+ */
+size_t hisa_block_attn_workspace_bytes(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb);
+int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int32_t* q_seq,
+                    const int32_t* q_pos, int n_q, const int32_t* blocks, int mb, int B, float scale,
+                    uint16_t* out, float* lse, void* ws, size_t ws_bytes, hisa_stream_t stream);
+
+/*
  * hisa_merge_topk — top-k of several (id, score) lists per row, by (score
  * desc, id asc): the exchange step of context parallelism.  ids and scores
  * are [lists, rows, n] (device, row-major; the layout an all-gather in list
@@ -486,7 +644,10 @@ enum hisa_phase {
     HISA_PHASE_QSPLIT = 9,        /* query heads split for fp8 scoring (e4m3 keys, d = 128) */
     HISA_PHASE_MERGE = 10,        /* hisa_merge_topk */
     HISA_PHASE_ATTN = 11,         /* hisa_sparse_attn */
-    HISA_NUM_PHASES = 12
+    HISA_PHASE_ROPE = 12,         /* hisa_rope */
+    HISA_PHASE_CACHE = 13,        /* hisa_cache_store, hisa_cache_load */
+    HISA_PHASE_BLOCK_ATTN = 14,   /* hisa_block_attn */
+    HISA_NUM_PHASES = 15
 };
 int hisa_profile_enable(int on);
 int hisa_profile_read(float* ms, int* launches, int reset);
