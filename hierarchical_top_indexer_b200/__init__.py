@@ -647,36 +647,45 @@ def hisa_sparse_attn(Qa: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lens: t
 class _on:
     """The device of a call's tensors current, and `stream` (default: that
     device's current stream) the one that buffers made by the call belong to."""
+    __slots__ = ("device", "stream", "_dev", "_str")
 
     def __init__(self, device, stream=None):
-        self.device, self.given = device, stream
+        self.device, self.stream, self._dev, self._str = device, stream, None, None
 
     def __enter__(self):
-        self._dev = torch.cuda.device(self.device)
-        self._dev.__enter__()
-        self._str = torch.cuda.stream(self.given if self.given is not None else torch.cuda.current_stream())
+        if self.device.index != torch.cuda.current_device():
+            self._dev = torch.cuda.device(self.device)
+            self._dev.__enter__()
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        self._str = torch.cuda.stream(self.stream)
         self._str.__enter__()
-        return _stream()
+        return self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        self._str.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        if self._str is not None:
+            self._str.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
 
 
 def _want(fn: str, name: str, t, dtype, device, shape):
     """The library sees pointers only: a tensor of another type, device, shape
     or layout than the call reads is refused here.  -1 in shape: any size."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.device != device or \
-            t.dim() != len(shape) or any(w >= 0 and n != w for n, w in zip(t.shape, shape)):
-        dims = ", ".join("*" if w < 0 else str(w) for w in shape)
-        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor [{dims}] on {device}")
-    return t
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous() and \
+                (t.shape == shape or (len(t.shape) == len(shape) and all(w < 0 or n == w for n, w in zip(t.shape, shape)))):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    dims = ", ".join("*" if w < 0 else str(w) for w in shape)
+    raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor [{dims}] on {device}")
 
 
 def _want_ws(fn: str, ws: torch.Tensor, device):
     if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
         raise ValueError(f"{fn}: ws must be a contiguous uint8 tensor on {device}")
-    return ws
+    return ws.data_ptr()
 
 
 def hisa_select_blocks_workspace_bytes(kv: KVCache, n_q: int, H: int, m: int) -> int:
@@ -733,16 +742,16 @@ def hisa_rope(plan: hisa_rope_plan, x: torch.Tensor, pos: torch.Tensor, out: Opt
     fn = "hisa_rope"
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x must be a CUDA tensor [rows, heads, d] or [rows, d]")
-    rows, heads = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
-    _want(fn, "x", x, torch.bfloat16, x.device, (*x.shape[:-1], plan.d))
-    _want(fn, "pos", pos, torch.int32, x.device, (rows,))
-    with _on(x.device, stream) as s:
+    dev, shape = x.device, x.shape
+    rows, heads = shape[0], 1 if len(shape) == 2 else shape[1]
+    xp = _want(fn, "x", x, torch.bfloat16, dev, (*shape[:-1], plan.d))
+    pp = _want(fn, "pos", pos, torch.int32, dev, (rows,))
+    with _on(dev, stream) as s:
         out = torch.empty_like(x) if out is None else out
-        _want(fn, "out", out, torch.bfloat16, x.device, tuple(x.shape))
-        if out.data_ptr() != x.data_ptr() and x.numel() and \
-                abs(out.data_ptr() - x.data_ptr()) < x.numel() * x.element_size():
+        yp = _want(fn, "out", out, torch.bfloat16, dev, shape)
+        if yp != xp and abs(yp - xp) < x.numel() * 2:
             raise ValueError(f"{fn}: out overlaps x without being x")
-        _check(fn, _lib.hisa_rope(ctypes.byref(plan), _ptr(x), _ptr(out), _ptr(pos), rows, heads, int(transpose), s))
+        _check(fn, _lib.hisa_rope(plan, xp, yp, pp, rows, heads, 1 if transpose else 0, s))
     return out
 
 
@@ -806,10 +815,7 @@ class AttnCache:
             k=ptr(k), v=ptr(v), k_scale=ptr(ks), v_scale=ptr(vs), len=ptr(lens), status=ptr(status), batch=self.batch,
             cap=self.cap, heads=self.heads, d=self.d, dtype=HISA_CACHE_FP4 if fp4 else HISA_CACHE_BF16,
             k_mul=self.k_mul, v_mul=self.v_mul)
-
-    @property
-    def struct(self):
-        return ctypes.byref(self._struct)
+        self.struct = ctypes.pointer(self._struct)
 
     def status_bits(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF
@@ -819,35 +825,34 @@ class AttnCache:
 
 
 def _cache_names(fn, c, seq, pos):
-    _want(fn, "seq", seq, torch.int32, c.device, (-1,))
-    if pos is not None:
-        _want(fn, "pos", pos, torch.int32, c.device, (seq.shape[0],))
-    return seq.shape[0]
+    sp = _want(fn, "seq", seq, torch.int32, c.device, (-1,))
+    n = seq.shape[0]
+    return n, sp, None if pos is None else _want(fn, "pos", pos, torch.int32, c.device, (n,))
 
 
 def hisa_cache_store(c: AttnCache, K: torch.Tensor, V: torch.Tensor, seq: torch.Tensor,
                      pos: Optional[torch.Tensor] = None, stream=None):
     """Tokens' key and value rows K, V [n, heads, d] bf16 into the cache at
     (seq[i], pos[i]); pos None: each sequence's last position len - 1."""
-    fn = "hisa_cache_store"
-    n = _cache_names(fn, c, seq, pos)
-    for name, t in (("K", K), ("V", V)):
-        _want(fn, name, t, torch.bfloat16, c.device, (n, c.heads, c.d))
-    with _on(c.device, stream) as s:
-        _check(fn, _lib.hisa_cache_store(c.struct, _ptr(K), _ptr(V), _ptr(seq), _ptr(pos), n, s))
+    fn, dev = "hisa_cache_store", c.device
+    n, sp, pp = _cache_names(fn, c, seq, pos)
+    shape = (n, c.heads, c.d)
+    kp, vp = _want(fn, "K", K, torch.bfloat16, dev, shape), _want(fn, "V", V, torch.bfloat16, dev, shape)
+    with _on(dev, stream) as s:
+        _check(fn, _lib.hisa_cache_store(c.struct, kp, vp, sp, pp, n, s))
 
 
 def hisa_cache_load(c: AttnCache, seq: torch.Tensor, pos: Optional[torch.Tensor] = None,
                     K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
     """The values (K, V) [n, heads, d] bf16 that the rows at (seq[i], pos[i]) stand for."""
-    fn = "hisa_cache_load"
-    n = _cache_names(fn, c, seq, pos)
-    with _on(c.device, stream) as s:
-        K = torch.empty((n, c.heads, c.d), dtype=torch.bfloat16, device=c.device) if K is None else K
-        V = torch.empty((n, c.heads, c.d), dtype=torch.bfloat16, device=c.device) if V is None else V
-        for name, t in (("K", K), ("V", V)):
-            _want(fn, name, t, torch.bfloat16, c.device, (n, c.heads, c.d))
-        _check(fn, _lib.hisa_cache_load(c.struct, _ptr(K), _ptr(V), _ptr(seq), _ptr(pos), n, s))
+    fn, dev = "hisa_cache_load", c.device
+    n, sp, pp = _cache_names(fn, c, seq, pos)
+    shape = (n, c.heads, c.d)
+    with _on(dev, stream) as s:
+        K = torch.empty(shape, dtype=torch.bfloat16, device=dev) if K is None else K
+        V = torch.empty(shape, dtype=torch.bfloat16, device=dev) if V is None else V
+        kp, vp = _want(fn, "K", K, torch.bfloat16, dev, shape), _want(fn, "V", V, torch.bfloat16, dev, shape)
+        _check(fn, _lib.hisa_cache_load(c.struct, kp, vp, sp, pp, n, s))
     return K, V
 
 
@@ -864,27 +869,26 @@ def hisa_block_attn(c: AttnCache, Qa: torch.Tensor, q_seq: torch.Tensor, q_pos: 
     blocks [n_q, mb] of B tokens (blocks None: the whole prefix), up to each
     row's position.  Returns (out [n_q, Hq, d] bf16, lse [n_q, Hq] fp32)."""
     fn, dev = "hisa_block_attn", c.device
-    _want(fn, "Qa", Qa, torch.bfloat16, dev, (-1, -1, c.d))
-    n_q, Hq = Qa.shape[0], Qa.shape[1]
-    _want(fn, "q_seq", q_seq, torch.int32, dev, (n_q,))
-    if q_pos is not None:
-        _want(fn, "q_pos", q_pos, torch.int32, dev, (n_q,))
+    qp = _want(fn, "Qa", Qa, torch.bfloat16, dev, (-1, -1, c.d))
+    n_q, Hq, d = Qa.shape
+    sp = _want(fn, "q_seq", q_seq, torch.int32, dev, (n_q,))
+    pp = None if q_pos is None else _want(fn, "q_pos", q_pos, torch.int32, dev, (n_q,))
+    mb, bp = 0, None
     if blocks is not None:
-        _want(fn, "blocks", blocks, torch.int32, dev, (n_q, -1))
-        if blocks.shape[1] < 1:
+        bp = _want(fn, "blocks", blocks, torch.int32, dev, (n_q, -1))
+        mb = blocks.shape[1]
+        if mb < 1:
             raise ValueError(f"{fn}: blocks must have a column (None: the whole prefix)")
-    mb = 0 if blocks is None else blocks.shape[1]
-    scale = (1.0 / c.d ** 0.5) if scale is None else float(scale)
+    scale = (1.0 / d ** 0.5) if scale is None else float(scale)
     with _on(dev, stream) as s:
         if ws is None:
             ws = workspace(hisa_block_attn_workspace_bytes(c, n_q, Hq, B, mb), dev)
-        _want_ws(fn, ws, dev)
-        out = torch.empty((n_q, Hq, c.d), dtype=torch.bfloat16, device=dev) if out is None else out
+        wp = _want_ws(fn, ws, dev)
+        out = torch.empty((n_q, Hq, d), dtype=torch.bfloat16, device=dev) if out is None else out
         lse = torch.empty((n_q, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        _want(fn, "out", out, torch.bfloat16, dev, (n_q, Hq, c.d))
-        _want(fn, "lse", lse, torch.float32, dev, (n_q, Hq))
-        _check(fn, _lib.hisa_block_attn(c.struct, _ptr(Qa), Hq, _ptr(q_seq), _ptr(q_pos), n_q, _ptr(blocks), mb, B,
-                                        scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s))
+        op = _want(fn, "out", out, torch.bfloat16, dev, (n_q, Hq, d))
+        lp = _want(fn, "lse", lse, torch.float32, dev, (n_q, Hq))
+        _check(fn, _lib.hisa_block_attn(c.struct, qp, Hq, sp, pp, n_q, bp, mb, B, scale, op, lp, wp, ws.numel(), s))
     return out, lse
 
 

@@ -868,6 +868,20 @@ bool heads_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of 4-bit codes [rows, cap, bytes] with boxes of [1, box, bytes], the
+// 16-byte chunks of a row swizzled so that a warp can read a row per lane.
+bool codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cap, int bytes, uint32_t box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), cap, rows};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(bytes), cap * bytes};
+    const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(bytes), box, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1478,11 +1492,13 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
     CUtensorMap qm, km, vm;
     std::memset(&qm, 0, sizeof qm);
     km = vm = qm;
+    const uint64_t bh = static_cast<uint64_t>(c->batch) * c->heads;
     if (!fp4) {
-        const uint64_t bh = static_cast<uint64_t>(c->batch) * c->heads;
         if (!heads_map(&qm, Qa, n_q, Hq, c->d, p.R, p.G) || !heads_map(&km, c->k, bh, c->cap, c->d, 1, p.PB) ||
             !heads_map(&vm, c->v, bh, c->cap, c->d, 1, p.PB))
             return HISA_E_CUDA;
+    } else if (p.dec && (!codes_map(&km, c->k, bh, c->cap, c->d / 2, p.PB) || !codes_map(&vm, c->v, bh, c->cap, c->d / 2, p.PB))) {
+        return HISA_E_CUDA;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     PhaseScope ps(HISA_PHASE_BLOCK_ATTN, s);

@@ -14,8 +14,8 @@
 // keys then serves up to 128 (row, head) pairs instead of G.  plan_kernel
 // turns a group's lists into a sorted list of pieces (up to 128 tokens of one
 // block of one sequence), without duplicates; 128 / piece pieces make a tile.
-// scan_kernel adds the tiles up, and the persistent CTAs of battn_kernel take
-// equal runs of all (key head, group, tile) slots.  A run's part of a group is
+// The persistent CTAs of battn_kernel add the groups' tiles up and take equal
+// runs of all (key head, group, tile) slots.  A run's part of a group is
 // a segment; a group that one segment covers is finished in place, the parts
 // of a group that several CTAs share are joined by join_kernel.
 //
@@ -37,7 +37,7 @@
 // P is rounded to bf16 (2^-8 relative) or f16 (2^-11); everything else is fp32.
 // f16 P is kept 2^7 larger, so that weights down to 2^-21 of the largest keep
 // all their bits and only those below 2^-32 of it vanish.
-#include "hisa_kernels.cuh"
+#include "battn.cuh"
 
 namespace hisa {
 
@@ -47,7 +47,6 @@ constexpr int kBaSoftWarps = 8;
 constexpr int kBaWarpLoad = 8;
 constexpr int kBaWarpMma = 9;
 constexpr int kBaWarpDeq = 10;      // 10-13 (4-bit rows)
-constexpr float kBaGrow = 8.f;      // log2 of how far a maximum may outgrow its reference
 
 template <int D, bool FP4>
 struct BaLayout {
@@ -68,39 +67,10 @@ struct BaLayout {
     static constexpr int threads = FP4 ? 448 : 320;
 };
 
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
-    tmem_ld16_nowait(taddr, r);
-    tmem_ld16_nowait(taddr + 16, r + 16);
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]^T, f16 or bf16 inputs, fp32 accumulate.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // M = 128, N = n, fp32 accumulate; f16 or bf16 inputs; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_ba(uint32_t n, bool f16, bool b_mn_major) {
     return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn_major ? (1u << 16) : 0u) | ((n >> 3) << 17) |
            ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ bool warp_wait_b(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    __syncwarp();
-    return ok;
 }
 
 // ------------------------------------------------------------------- plan
@@ -199,96 +169,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const BattnParams p)
     }
     if (tid == 0) {
         p.pieces[g] = base;
-        p.tile0[g + 1] = (base + p.S - 1) / p.S;   // turned into sums by scan_kernel
-        if (g == 0) p.tile0[0] = 0;
-    }
-}
-
-// tile0[g + 1] = tiles of groups 0..g (one CTA).
-__global__ void __launch_bounds__(1024) scan_kernel(int* tile0, int groups) {
-    __shared__ int s_w[32];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int carry = 0;
-    for (int g0 = 0; g0 < groups; g0 += 1024) {
-        int x = g0 + tid < groups ? tile0[g0 + tid + 1] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) s_w[warp] = x;
-        __syncthreads();
-        int before = carry, all = 0;
-        for (int q = 0; q < 32; ++q) {
-            if (q < warp) before += s_w[q];
-            all += s_w[q];
-        }
-        if (g0 + tid < groups) tile0[g0 + tid + 1] = before + x;
-        carry += all;
-        __syncthreads();
+        p.tiles[g] = (base + p.S - 1) / p.S;
     }
 }
 
 // -------------------------------------------------------------- attention
-
-// A run's place: key head h, group g, tiles [t0, t0 + n) of the group's T.
-struct BaSeg {
-    int h, g, t0, n, T;
-};
-
-struct BaCursor {
-    long long at, end;
-    int h, g;
-
-    // The run [at, end) of the whole warp's CTA (all lanes call this).
-    __device__ __forceinline__ void start(const BattnParams& p, int tot) {
-        const int lane = threadIdx.x & 31;
-        const long long all = static_cast<long long>(tot) * p.Hkv;
-        // CTAs past the number of tiles have none, so that no CTA between two others is idle
-        const long long n = min(static_cast<long long>(gridDim.x), all), c = min(static_cast<long long>(blockIdx.x), n);
-        at = n > 0 ? all * c / n : 0;
-        end = n > 0 ? all * min(c + 1, n) / n : 0;
-        h = at < end ? static_cast<int>(at / tot) : 0;
-        const int x = at < end ? static_cast<int>(at - static_cast<long long>(h) * tot) : 0;
-        // the group with tile0[g] <= x < tile0[g + 1]: 32 probes a step
-        int lo = 0, hi = p.groups;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32;
-            const int probe = lo + (lane + 1) * step;
-            const bool below = probe < hi && __ldcg(p.tile0 + probe) <= x;
-            const int hits = __popc(__ballot_sync(0xffffffffu, below));
-            const int lo2 = lo + hits * step;
-            hi = min(hi, lo2 + step);
-            lo = lo2;
-        }
-        g = lo;
-    }
-
-    __device__ __forceinline__ bool next(const BattnParams& p, int tot, BaSeg* s) {
-        if (at >= end) return false;
-        const int x = static_cast<int>(at - static_cast<long long>(h) * tot);
-        int b0 = __ldcg(p.tile0 + g), b1 = __ldcg(p.tile0 + g + 1);
-        while (b1 == b0 || x >= b1) {   // empty groups
-            ++g;
-            b0 = b1;
-            b1 = __ldcg(p.tile0 + g + 1);
-        }
-        s->h = h;
-        s->g = g;
-        s->t0 = x - b0;
-        s->T = b1 - b0;
-        const long long left = end - at;
-        s->n = left < b1 - x ? static_cast<int>(left) : b1 - x;
-        at += s->n;
-        if (x + s->n == tot) {
-            ++h;
-            g = 0;
-        }
-        return true;
-    }
-};
 
 template <int D, bool FP4>
 __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
@@ -351,9 +236,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const int tot = __ldcg(p.tile0 + p.groups);
-    BaCursor cur;
-    cur.start(p, tot);
+    BaCursor cur = ba_start(p, reinterpret_cast<int*>(smem + L::ml));
     BaSeg sg;
     bool ok = true;
 
@@ -361,7 +244,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         // ------------------------------------------------------------ load
         // Lane s < S loads piece s of each tile.
         uint32_t it = 0, seg = 0, issued[2] = {0, 0};
-        while (ok && cur.next(p, tot, &sg)) {
+        while (ok && cur.next(p, &sg)) {
             const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
             const int np = p.pieces[sg.g];
             if (!FP4) {
@@ -446,7 +329,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         const uint32_t aq = smem_addr(smem + L::q);
         uint32_t kn = 0, vn = 0, seg = 0, pn0 = 0, pn1 = 0;
         if (lane == 0) {
-            while (ok && cur.next(p, tot, &sg)) {
+            while (ok && cur.next(p, &sg)) {
                 auto issue_s = [&](int j) -> bool {
                     const uint32_t slot = kn % kR;
                     if (!mbar_wait(kfull + slot, (kn / kR) & 1, abort_flag)) return false;
@@ -511,7 +394,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         float2* ml = reinterpret_cast<float2*>(smem + L::ml);
         const float* qs = reinterpret_cast<const float*>(smem + L::qs);
         uint32_t sn = 0, seg = 0, vbase = 0;
-        while (ok && cur.next(p, tot, &sg)) {
+        while (ok && cur.next(p, &sg)) {
             const int row = sg.g * p.R + rr;
             const bool live = rr < p.R && row < p.n_q;
             int b = -1, t = -1;
@@ -693,7 +576,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         // ------------------------------------------------------ dequantise
         const int dw = warp - kBaWarpDeq;
         uint32_t it = 0, seg = 0;
-        while (ok && cur.next(p, tot, &sg)) {
+        while (ok && cur.next(p, &sg)) {
             const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
             const int np = p.pieces[sg.g];
             if (seg > 0 && !(ok = warp_wait_b(qempty, (seg - 1) & 1, abort_flag))) break;
@@ -829,7 +712,7 @@ __global__ void __launch_bounds__(256) join_kernel(const BattnParams p, int grid
         if (c0 == c1) return;   // finished in place
         for (int c = c0 + lane; c <= c1; c += 32) {
             const int slot = 2 * c + (c == c0 ? 1 : 0);
-            M = fmaxf(M, p.part_ml[slot * 128 + r].x);
+            M = fmaxf(M, p.part_ml[slot * p.prow + r].x);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -837,7 +720,7 @@ __global__ void __launch_bounds__(256) join_kernel(const BattnParams p, int grid
             const int c = cb + lane;
             float w = 0.f;
             if (c <= c1) {
-                const float2 v = p.part_ml[(2 * c + (c == c0 ? 1 : 0)) * 128 + r];
+                const float2 v = p.part_ml[(2 * c + (c == c0 ? 1 : 0)) * p.prow + r];
                 w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
                 Ls += w * v.y;
             }
@@ -846,7 +729,7 @@ __global__ void __launch_bounds__(256) join_kernel(const BattnParams p, int grid
             for (int k = 0; k < some; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, w, k);
                 const int ck = cb + k;
-                const float* po = p.part_o + (static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * 128 + r) * D + lane * E;
+                const float* po = p.part_o + (static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * p.prow + r) * D + lane * E;
                 if (E == 4) {
                     const float4 v = *reinterpret_cast<const float4*>(po);
                     acc[0] += wk * v.x;
@@ -895,15 +778,14 @@ cudaError_t launch_typed(const CUtensorMap& qm, const CUtensorMap& km, const CUt
     cfg.dynamicSmemBytes = bits;
     e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, scan_kernel, p.tile0, p.groups);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(L::threads);
-    cfg.dynamicSmemBytes = L::total;
-    e = cudaLaunchKernelEx(&cfg, battn_kernel<D, FP4>, qm, km, vm, p);
+    if (p.dec) {
+        e = launch_battn_dec(qm, km, vm, p, FP4, grid, s);
+    } else {
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(L::threads);
+        cfg.dynamicSmemBytes = L::total;
+        e = cudaLaunchKernelEx(&cfg, battn_kernel<D, FP4>, qm, km, vm, p);
+    }
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * p.Hkv, static_cast<unsigned>((p.R * p.G + 7) / 8));
     cfg.blockDim = dim3(256);
@@ -939,16 +821,21 @@ size_t battn_layout(BattnParams& p, void* ws) {
     };
     p.list = reinterpret_cast<int2*>(take(static_cast<size_t>(p.groups) * lcap * 8));
     p.pieces = reinterpret_cast<int*>(take(static_cast<size_t>(p.groups) * 4));
+    p.tiles = reinterpret_cast<int*>(take(static_cast<size_t>(p.groups) * 4));
     p.tile0 = reinterpret_cast<int*>(take(static_cast<size_t>(p.groups + 1) * 4));
     p.bits = reinterpret_cast<uint32_t*>(take(p.R > 1 ? static_cast<size_t>(p.n_q) * p.W * 4 : 0));
-    p.part_o = reinterpret_cast<float*>(take(static_cast<size_t>(2) * kBattnMaxGrid * 128 * p.d * 4));
-    p.part_ml = reinterpret_cast<float2*>(take(static_cast<size_t>(2) * kBattnMaxGrid * 128 * 8));
+    // a lone row with few heads: tokens in the MMA's rows, two CTAs per SM
+    p.dec = p.R == 1 && p.G <= kBattnDecHeads;
+    p.prow = p.dec ? kBattnDecHeads : 128;
+    const size_t parts = static_cast<size_t>(2) * kBattnMaxSms * (p.dec ? 2 : 1) * p.prow;
+    p.part_o = reinterpret_cast<float*>(take(parts * p.d * 4));
+    p.part_ml = reinterpret_cast<float2*>(take(parts * 8));
     return off;
 }
 
 cudaError_t launch_battn(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const BattnParams& p, bool fp4,
                          int sms, cudaStream_t s) {
-    const int grid = sms < kBattnMaxGrid ? sms : kBattnMaxGrid;
+    const int grid = (sms < kBattnMaxSms ? sms : kBattnMaxSms) * (p.dec ? 2 : 1);
     if (fp4)
         return p.d == 128 ? launch_typed<128, true>(qm, km, vm, p, grid, s) : launch_typed<64, true>(qm, km, vm, p, grid, s);
     return p.d == 128 ? launch_typed<128, false>(qm, km, vm, p, grid, s) : launch_typed<64, false>(qm, km, vm, p, grid, s);

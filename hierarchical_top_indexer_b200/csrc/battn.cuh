@@ -1,0 +1,125 @@
+// What the two block-attention kernels share (battn.cu: up to 128 (row, head)
+// pairs per tile; battn_dec.cu: single rows with few heads): a CTA's place in
+// the list of tiles, and tcgen05 forms.
+#pragma once
+
+#include "hisa_kernels.cuh"
+
+namespace hisa {
+
+constexpr float kBaGrow = 8.f;      // log2 of how far a maximum may outgrow its reference
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, f16 or bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ bool warp_wait_b(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    __syncwarp();
+    return ok;
+}
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+    tmem_ld16_nowait(taddr, r);
+    tmem_ld16_nowait(taddr + 16, r + 16);
+}
+
+// A run's place: key head h, group g, tiles [t0, t0 + n) of the group's T.
+struct BaSeg {
+    int h, g, t0, n, T;
+};
+
+// The CTA's run [at, end) of all (key head, group, tile) slots; b0: tiles of
+// the groups before g.
+struct BaCursor {
+    long long at, end;
+    int tot, h, g, b0;
+
+    __device__ __forceinline__ bool next(const BattnParams& p, BaSeg* s) {
+        if (at >= end) return false;
+        const int x = static_cast<int>(at - static_cast<long long>(h) * tot);
+        int T = __ldcg(p.tiles + g);
+        while (x >= b0 + T) {   // done with, or empty
+            b0 += T;
+            T = __ldcg(p.tiles + ++g);
+        }
+        s->h = h;
+        s->g = g;
+        s->t0 = x - b0;
+        s->T = T;
+        const long long left = end - at;
+        s->n = left < b0 + T - x ? static_cast<int>(left) : b0 + T - x;
+        at += s->n;
+        if (x + s->n == tot) {
+            ++h;
+            g = b0 = 0;
+        }
+        return true;
+    }
+};
+
+// Every thread of the CTA: adds the groups' tiles up and finds the run's
+// start.  scratch: 40 ints of shared memory.  CTA 0 leaves the sums in tile0
+// for join_kernel.
+__device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch) {
+    const int tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (p.groups + n - 1) / n;
+    const int g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
+    int sum = 0;
+    for (int g = g0; g < g1; ++g) sum += __ldcg(p.tiles + g);
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    BaCursor c;
+    int before = x - sum;
+    c.tot = 0;
+    for (int w = 0; w < n / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        c.tot += scratch[w];
+    }
+    // CTAs past the number of slots have none, so that no CTA between two others is idle
+    const long long all = static_cast<long long>(c.tot) * p.Hkv;
+    const long long ctas = min(static_cast<long long>(gridDim.x), all), i = min(static_cast<long long>(blockIdx.x), ctas);
+    c.at = ctas > 0 ? all * i / ctas : 0;
+    c.end = ctas > 0 ? all * min(i + 1, ctas) / ctas : 0;
+    c.h = c.at < c.end ? static_cast<int>(c.at / c.tot) : 0;
+    const int at = c.at < c.end ? static_cast<int>(c.at - static_cast<long long>(c.h) * c.tot) : 0;
+    if (blockIdx.x == 0) {
+        int b = before;
+        if (tid == 0) p.tile0[0] = 0;
+        for (int g = g0; g < g1; ++g) p.tile0[g + 1] = b += __ldcg(p.tiles + g);
+    }
+    if (sum > 0 && at >= before && at < before + sum) {
+        int g = g0, b = before;
+        while (at >= b + __ldcg(p.tiles + g)) b += __ldcg(p.tiles + g++);
+        scratch[32] = g;
+        scratch[33] = b;
+    }
+    if (c.tot == 0 && tid == 0) scratch[32] = scratch[33] = 0;
+    __syncthreads();
+    c.g = scratch[32];
+    c.b0 = scratch[33];
+    __syncthreads();   // the scratch is free again
+    return c;
+}
+
+}  // namespace hisa

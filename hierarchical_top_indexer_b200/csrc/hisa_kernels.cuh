@@ -250,7 +250,8 @@ cudaError_t launch_cache_store(const CacheParams& p, cudaStream_t s);
 cudaError_t launch_cache_load(const CacheParams& p, cudaStream_t s);
 
 // Block-sparse attention (battn.cu).
-constexpr int kBattnMaxGrid = 148;   // CTAs (one per SM) whose partial outputs the workspace holds
+constexpr int kBattnMaxSms = 148;    // SMs whose CTAs' partial outputs the workspace holds
+constexpr int kBattnDecHeads = 16;   // most heads per key head of the single-row kernel
 struct BattnParams {
     const uint16_t* q;       // [n_q, Hq, d] bf16
     const int32_t* q_seq;    // [n_q]
@@ -273,15 +274,19 @@ struct BattnParams {
     int W, lcap;             // words of a row's block bitmap, pieces a group's list holds
     int2* list;              // workspace: [groups, lcap]
     int* pieces;             // [groups]
-    int* tile0;              // [groups + 1] tiles of the groups before
+    int* tiles;              // [groups] tiles of each group
+    int* tile0;              // [groups + 1] tiles of the groups before (for join_kernel)
     uint32_t* bits;          // [n_q, W] (R > 1)
-    float* part_o;           // [2 * grid, 128, d]
-    float2* part_ml;         // [2 * grid, 128] maximum (log2 domain) and sum
+    int dec, prow;           // the single-row kernel serves the call; rows of a part
+    float* part_o;           // [2 * grid, prow, d]
+    float2* part_ml;         // [2 * grid, prow] maximum (log2 domain) and sum
 };
 // Fills in the derived sizes and the workspace pointers; returns the bytes.
 size_t battn_layout(BattnParams& p, void* ws);
 cudaError_t launch_battn(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                          const BattnParams& p, bool fp4, int sms, cudaStream_t s);
+cudaError_t launch_battn_dec(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             const BattnParams& p, bool fp4, int grid, cudaStream_t s);
 
 // One warp waiting on an mbarrier that never completes (diag.cu).
 cudaError_t launch_wait_probe(uint32_t* status, cudaStream_t s);
