@@ -313,76 +313,79 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
             // the copies in flight land before the CTA gives up its shared memory
             volatile int keep_waiting = 0;
             if (!FP4) {
-                if (seg > 0) mbar_wait(qfull, (seg - 1) & 1, &keep_waiting);
+                if (seg > 0) ba_wait(qfull, (seg - 1) & 1, &keep_waiting);
                 for (int kv = 0; kv < 2; ++kv)
                     for (uint32_t i = issued[kv] > kR ? issued[kv] - kR : 0; i < issued[kv]; ++i)
-                        mbar_wait((kv ? vfull : kfull) + i % kR, (i / kR) & 1, &keep_waiting);
+                        ba_wait((kv ? vfull : kfull) + i % kR, (i / kR) & 1, &keep_waiting);
             } else {
                 constexpr uint32_t n = kRaw ? kRaw : 1;
                 for (uint32_t i = issued[0] > n ? issued[0] - n : 0; i < issued[0]; ++i)
-                    mbar_wait(rfull + i % n, (i / n) & 1, &keep_waiting);
+                    ba_wait(rfull + i % n, (i / n) & 1, &keep_waiting);
             }
         }
     } else if (warp == kBaWarpMma) {
         // ------------------------------------------------------------- MMA
         constexpr uint32_t id_s = idesc_ba(128, FP4, false), id_o = idesc_ba(D, FP4, true);
-        const uint32_t aq = smem_addr(smem + L::q);
-        uint32_t kn = 0, vn = 0, seg = 0, pn0 = 0, pn1 = 0;
-        if (lane == 0) {
-            while (ok && cur.next(p, &sg)) {
-                auto issue_s = [&](int j) -> bool {
-                    const uint32_t slot = kn % kR;
-                    if (!mbar_wait(kfull + slot, (kn / kR) & 1, abort_flag)) return false;
-                    tc_fence_after();
-                    const uint32_t bk = smem_addr(smem + L::k0) + slot * L::tile;
+        const uint32_t q_lo = uni(desc_lo(smem_addr(smem + L::q), 16)), k_lo = uni(desc_lo(smem_addr(smem + L::k0), 16));
+        const uint32_t v_lo = uni(desc_lo(smem_addr(smem + L::v0), 16384)), tm = uni(tmem_base);
+        uint32_t kn = 0, vn = 0, seg = 0, pn[2] = {0, 0};
+        auto issue_s = [&](int j) -> bool {
+            const uint32_t slot = kn % kR;
+            if (!warp_wait_b(kfull + slot, (kn / kR) & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t td = uni(tm + (j & 1) * 128), b = uni(k_lo + slot * (L::tile >> 4));
+            if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t o = (s >> 2) * 16384 + (s & 3) * 32;
-                        umma_bf16(tmem_base + (j & 1) * 128, sw128_kmajor_desc(aq + o), sw128_kmajor_desc(bk + o), id_s, s > 0);
-                    }
-                    umma_commit(kempty + slot);
-                    umma_commit(sfull + (j & 1));
-                    ++kn;
-                    return true;
-                };
-                ok = mbar_wait(qfull, seg & 1, abort_flag);
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s >> 2) * (16384 >> 4) + (s & 3) * 2;
+                    umma_bf16(td, desc64(q_lo + o, kHi128), desc64(b + o, kHi128), id_s, s > 0);
+                }
+                umma_commit(kempty + slot);
+                umma_commit(sfull + (j & 1));
+            }
+            __syncwarp();
+            ++kn;
+            return true;
+        };
+        while (ok && cur.next(p, &sg)) {
+            if (!(ok = warp_wait_b(qfull, seg & 1, abort_flag))) break;
+            tc_fence_after();
+            ok = issue_s(0) && (sg.n < 2 || issue_s(1));
+            if (ok && sg.n <= 2 && elect_one()) umma_commit(qempty);
+            for (int j = 0; j < sg.n && ok; ++j) {
+                ok = warp_wait_b(pfull + (j & 1), pn[j & 1] & 1, abort_flag);
+                ++pn[j & 1];
+                if (ok && j == 0 && seg > 0) ok = warp_wait_b(oempty, (seg - 1) & 1, abort_flag);
+                const uint32_t slot = vn % kR;
+                ok = ok && warp_wait_b(vfull + slot, (vn / kR) & 1, abort_flag);
                 if (!ok) break;
-                ok = issue_s(0) && (sg.n < 2 || issue_s(1));
-                if (ok && sg.n <= 2) umma_commit(qempty);
-                for (int j = 0; j < sg.n && ok; ++j) {
-                    uint32_t& pn = (j & 1) ? pn1 : pn0;
-                    ok = mbar_wait(pfull + (j & 1), pn & 1, abort_flag);
-                    ++pn;
-                    if (ok && j == 0 && seg > 0) ok = mbar_wait(oempty, (seg - 1) & 1, abort_flag);
-                    const uint32_t slot = vn % kR;
-                    if (ok) ok = mbar_wait(vfull + slot, (vn / kR) & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t bv = smem_addr(smem + L::v0) + slot * L::tile;
+                tc_fence_after();
+                const uint32_t ta = uni(tm + (j & 1) * 128), b = uni(v_lo + slot * (L::tile >> 4)), more = uni(j > 1 ? 1u : 0u);
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        umma_f16_ts(tmem_base + 256 + (j & 1) * 128, tmem_base + (j & 1) * 128 + s * 8,
-                                    sw128_mnmajor_desc(bv + s * 2048), id_o, (j > 1 || s > 0) ? 1u : 0u);
+                        umma_f16_ts(ta + 256, ta + s * 8, desc64(b + s * (2048 >> 4), kHi128), id_o, s > 0 ? 1u : more);
                     umma_commit(vempty + slot);
-                    ++vn;
-                    if (j + 2 < sg.n) {
-                        ok = issue_s(j + 2);
-                        if (j + 3 == sg.n) umma_commit(qempty);
-                    }
+                    if (j + 1 == sg.n) umma_commit(odone);
                 }
-                if (ok) umma_commit(odone);
-                ++seg;
+                __syncwarp();
+                ++vn;
+                if (j + 2 < sg.n) {
+                    ok = issue_s(j + 2);
+                    if (j + 3 == sg.n && elect_one()) umma_commit(qempty);
+                }
             }
-            if (!ok) {
-                *abort_flag = 1;
-                set_status(p.status, HISA_DEV_TIMEOUT);
-            }
-            // every MMA done before TMEM is freed (a bounded wait that an abort does not cut short)
-            volatile int keep_waiting = 0;
-            umma_commit(done);
-            if (!mbar_wait(done, 0, &keep_waiting)) set_status(p.status, HISA_DEV_TIMEOUT);
+            ++seg;
         }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            set_status(p.status, HISA_DEV_TIMEOUT);
+        }
+        // every MMA done before TMEM is freed (a bounded wait that an abort does not cut short)
+        volatile int keep_waiting = 0;
+        if (elect_one()) umma_commit(done);
         __syncwarp();
+        if (!warp_wait_b(done, 0, &keep_waiting) && lane == 0) set_status(p.status, HISA_DEV_TIMEOUT);
     } else if (warp < kBaSoftWarps) {
         // --------------------------------------------------------- softmax
         const int set = warp >> 2, quad = warp & 3;
@@ -835,7 +838,7 @@ size_t battn_layout(BattnParams& p, void* ws) {
 
 cudaError_t launch_battn(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const BattnParams& p, bool fp4,
                          int sms, cudaStream_t s) {
-    const int grid = (sms < kBattnMaxSms ? sms : kBattnMaxSms) * (p.dec ? 2 : 1);
+    const int grid = (sms < kBattnMaxSms ? sms : kBattnMaxSms) * (p.dec && !fp4 ? 2 : 1);   // CTAs per SM
     if (fp4)
         return p.d == 128 ? launch_typed<128, true>(qm, km, vm, p, grid, s) : launch_typed<64, true>(qm, km, vm, p, grid, s);
     return p.d == 128 ? launch_typed<128, false>(qm, km, vm, p, grid, s) : launch_typed<64, false>(qm, km, vm, p, grid, s);

@@ -25,18 +25,66 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// mbar_wait for pipelines whose waits are mostly short: the timer that bounds
+// the wait is read only once 64 polls have failed, since a read takes longer
+// than such a wait.
+__device__ __forceinline__ bool ba_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const uint32_t a = smem_addr(bar);
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(a, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (abort_flag && *abort_flag) return false;
+            const uint64_t t = global_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+
+// Lane 0 waits; the warp learns the outcome.
 __device__ __forceinline__ bool warp_wait_b(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag);
+    if ((threadIdx.x & 31) == 0) ok = ba_wait(bar, parity, abort_flag);
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     __syncwarp();
     return ok;
+}
+
+// 32 lanes x 32 bit, 4 consecutive columns per thread, without waiting.
+__device__ __forceinline__ void tmem_ld4_nowait(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
     tmem_ld16_nowait(taddr, r);
     tmem_ld16_nowait(taddr + 16, r + 16);
 }
+
+// Issuing MMAs: a thread that builds a 64-bit descriptor per instruction in a
+// divergent branch takes 120 to 170 cycles for each, more than the MMAs
+// themselves (22 to 64 cycles at M = 128, K = 16).  So the whole warp runs the
+// loop, one elected lane issues, the descriptors' upper halves are constants,
+// and their lower halves are made known to be the same in every lane, which
+// puts the additions on the uniform datapath.
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A descriptor's halves: start address and leading offset (bytes); stride
+// offset (bytes), version 1 and swizzle mode (2: 128 bytes, 6: 32 bytes).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) { return (saddr >> 4) | ((lead >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) { return (stride >> 4) | (1u << 14) | (swizzle << 29); }
+constexpr uint32_t kHi128 = desc_hi(1024, 2);   // both majors, 128-byte swizzle: 8-row groups 1 KB apart
+
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
 
 // A run's place: key head h, group g, tiles [t0, t0 + n) of the group's T.
 struct BaSeg {
