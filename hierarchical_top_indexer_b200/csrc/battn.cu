@@ -175,13 +175,85 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const BattnParams p)
 
 // -------------------------------------------------------------- attention
 
+// One MMA row (this thread's) of one tile: S (TMEM, 128 columns at ts) to P in
+// its place, with the row's reference m and sum l, and its output (TMEM, to)
+// rescaled if the reference moves.  MASK: element by element as mw says; else
+// the row is seen whole (on) or not at all.  first: nothing in O yet.
+template <int D, bool FP4, bool MASK>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const uint32_t (&mw)[4], bool on, bool first, float c2,
+                                             float& m, float& l) {
+    constexpr float kRef = FP4 ? 7.f : 0.f;   // log2 of the largest P of a fresh maximum
+    // S is read twice, 32 columns ahead of their use (all 128 would not fit the registers)
+    uint32_t v[2][32];
+    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    tmem_ld32_nowait(ts, v[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait();
+        if (c < 3) tmem_ld32_nowait(ts + (c + 1) * 32, v[(c + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!MASK || ((mw[c] >> i) & 1u)) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[c & 1][i]));
+    }
+    float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+    if (!MASK && !on) mx = -INFINITY;
+    if (mx > -INFINITY) mx *= c2;   // -inf where the row sees nothing
+    if (first) {
+        m = mx - kRef;
+    } else {
+        const bool grew = mx > m + (kRef + kBaGrow) || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, grew)) {
+            const float alpha = grew ? ex2_approx(m - (mx - kRef)) : 1.f;
+            if (grew) m = mx - kRef;
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t w[16];
+                tmem_ld16_nowait(to + c * 16, w);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+                tmem_st16(to + c * 16, w);
+            }
+        }
+    }
+    tmem_ld32_nowait(ts, v[0]);
+    const bool off = !MASK && !on;
+    const float mul = off ? 0.f : c2, sub = off ? -200.f : m == -INFINITY ? 0.f : -m;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t(&x)[32] = v[c & 1];
+        tmem_ld_wait();
+        if (c < 3) tmem_ld32_nowait(ts + (c + 1) * 32, v[(c + 1) & 1]);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float e[4] = {sub, sub, sub, sub};
+            fma2(e[0], e[1], mul, mul, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            fma2(e[2], e[3], mul, mul, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                e[u] = ex2_approx(e[u]);
+                if (MASK && !((mw[c] >> (i + u)) & 1u)) e[u] = 0.f;
+            }
+            fma2(s0, s1, 1.f, 1.f, e[0], e[1]);
+            fma2(s2, s3, 1.f, 1.f, e[2], e[3]);
+            w[i / 2] = FP4 ? pack_f16(e[0], e[1]) : pack_bf16(e[0], e[1]);
+            w[i / 2 + 1] = FP4 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
+        }
+        tmem_st16(ts + c * 16, w);
+    }
+    l += (s0 + s1) + (s2 + s3);
+    tmem_st_wait();
+}
+
 template <int D, bool FP4>
 __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
     battn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const BattnParams p) {
     using L = BaLayout<D, FP4>;
     constexpr int kR = L::rings, kRaw = L::raws;
-    constexpr float kRef = FP4 ? 7.f : 0.f;   // log2 of the largest P of a fresh maximum
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
     uint64_t* kfull = bars;             // [kR] K operand ready (bytes; 4-bit: 4 warps)
@@ -307,20 +379,21 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
                 }
             }
         }
-        if (!ok && lane == 0) {
-            *abort_flag = 1;
-            set_status(p.status, HISA_DEV_TIMEOUT);
+        if (!ok) {
+            if (lane == 0) {
+                *abort_flag = 1;
+                set_status(p.status, HISA_DEV_TIMEOUT);
+            }
             // the copies in flight land before the CTA gives up its shared memory
-            volatile int keep_waiting = 0;
             if (!FP4) {
-                if (seg > 0) ba_wait(qfull, (seg - 1) & 1, &keep_waiting);
+                if (seg > 0) warp_wait_b(qfull, (seg - 1) & 1, nullptr);
                 for (int kv = 0; kv < 2; ++kv)
                     for (uint32_t i = issued[kv] > kR ? issued[kv] - kR : 0; i < issued[kv]; ++i)
-                        ba_wait((kv ? vfull : kfull) + i % kR, (i / kR) & 1, &keep_waiting);
+                        warp_wait_b((kv ? vfull : kfull) + i % kR, (i / kR) & 1, nullptr);
             } else {
                 constexpr uint32_t n = kRaw ? kRaw : 1;
                 for (uint32_t i = issued[0] > n ? issued[0] - n : 0; i < issued[0]; ++i)
-                    ba_wait(rfull + i % n, (i / n) & 1, &keep_waiting);
+                    warp_wait_b(rfull + i % n, (i / n) & 1, nullptr);
             }
         }
     } else if (warp == kBaWarpMma) {
@@ -333,7 +406,8 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
             const uint32_t slot = kn % kR;
             if (!warp_wait_b(kfull + slot, (kn / kR) & 1, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t td = uni(tm + (j & 1) * 128), b = uni(k_lo + slot * (L::tile >> 4));
+            const uint32_t at = uni(slot * 2 + (j & 1));
+            const uint32_t td = tm + (at & 1) * 128, b = k_lo + (at >> 1) * (L::tile >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
@@ -360,7 +434,8 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
                 ok = ok && warp_wait_b(vfull + slot, (vn / kR) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ta = uni(tm + (j & 1) * 128), b = uni(v_lo + slot * (L::tile >> 4)), more = uni(j > 1 ? 1u : 0u);
+                const uint32_t at = uni(slot * 4 + (j > 1 ? 2 : 0) + (j & 1));
+                const uint32_t ta = tm + (at & 1) * 128, b = v_lo + (at >> 2) * (L::tile >> 4), more = (at >> 1) & 1;
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
@@ -382,10 +457,9 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
             set_status(p.status, HISA_DEV_TIMEOUT);
         }
         // every MMA done before TMEM is freed (a bounded wait that an abort does not cut short)
-        volatile int keep_waiting = 0;
         if (elect_one()) umma_commit(done);
         __syncwarp();
-        if (!warp_wait_b(done, 0, &keep_waiting) && lane == 0) set_status(p.status, HISA_DEV_TIMEOUT);
+        if (!warp_wait_b(done, 0, nullptr) && lane == 0) set_status(p.status, HISA_DEV_TIMEOUT);
     } else if (warp < kBaSoftWarps) {
         // --------------------------------------------------------- softmax
         const int set = warp >> 2, quad = warp & 3;
@@ -407,11 +481,16 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
             const uint32_t* bits = p.R > 1 && p.blocks && t >= 0 ? p.bits + static_cast<size_t>(row) * p.W : nullptr;
             float c2 = p.scale_log2;
             float m = -INFINITY, l = 0.f;
-            for (int j = set; j < sg.n; j += 2, ++sn) {
-                // which of the tile's 128 tokens this row sees
-                uint32_t mw[4] = {0u, 0u, 0u, 0u};
-                bool tail = false;   // a piece with tokens no row sees: its V rows may hold anything
+            // which of tile j's 128 tokens this row sees (every one in an MMA row without a
+            // query, so that it costs its warp nothing), and whether the tile has tokens that
+            // no row of the group sees
+            uint32_t mw[4];
+            bool tail = false;
+            auto look = [&](int j) {
+                mw[0] = mw[1] = mw[2] = mw[3] = live ? 0u : 0xffffffffu;
+                tail = false;
                 const int e0 = (sg.t0 + j) * p.S;
+#pragma unroll 1
                 for (int s = 0; s < p.S; ++s) {
                     if (e0 + s >= np) break;
                     const int2 pc = list[e0 + s];
@@ -429,7 +508,9 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
                         if (hi > lo) mw[w] |= (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
                     }
                 }
-                if (!live) mw[0] = mw[1] = mw[2] = mw[3] = 0xffffffffu;   // an unused MMA row must not cost its warp the masks
+            };
+            look(set);
+            for (int j = set; j < sg.n; j += 2, ++sn) {
                 if (!(ok = warp_wait_b(sfull + set, sn & 1, abort_flag))) break;
                 tc_fence_after();
                 if (FP4) c2 = qs[(seg & 1) * 128 + r];
@@ -437,8 +518,8 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
                     // V rows past the last token any row sees: zeros, for 0 * NaN is NaN
                     const uint32_t vi = vbase + j;
                     if (!(ok = warp_wait_b(vfull + vi % kR, (vi / kR) & 1, abort_flag))) break;
-                    const int s = r / p.PB;
-                    if (e0 + s < np && r - s * p.PB >= (list[e0 + s].x & 255)) {
+                    const int e = (sg.t0 + j) * p.S + r / p.PB;
+                    if (e < np && r % p.PB >= (list[e].x & 255)) {
                         uint8_t* v = smem + L::v0 + (vi % kR) * L::tile + r * 128;
                         for (int a = 0; a < D / 64; ++a)
 #pragma unroll
@@ -448,71 +529,29 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
                     fence_async_smem();
                 }
                 if (mine) {
-                    const bool full = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
-                    const bool all_full = __all_sync(0xffffffffu, full);
-                    uint32_t v[2][32];
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        tmem_ld32_nowait(ts + c * 32, v[0]);
-                        tmem_ld32_nowait(ts + c * 32 + 32, v[1]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (all_full || ((mw[c + u] >> i) & 1u)) mx = fmaxf(mx, __uint_as_float(v[u][i]));
-                    }
-                    if (mx > -INFINITY) mx *= c2;   // -inf where the row sees nothing
-                    if (j < 2) {
-                        m = mx - kRef;
-                    } else {
-                        const bool grew = mx > m + (kRef + kBaGrow) || (m == -INFINITY && mx > m);
-                        if (__any_sync(0xffffffffu, grew)) {
-                            const float alpha = grew ? ex2_approx(m - (mx - kRef)) : 1.f;
-                            if (grew) m = mx - kRef;
-                            l *= alpha;
-#pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
-                                float o[16];
-                                uint32_t w[16];
-                                tmem_ld16_nowait(to + c * 16, w);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    o[i] = __uint_as_float(w[i]) * alpha;
-                                    w[i] = __float_as_uint(o[i]);
-                                }
-                                tmem_st16(to + c * 16, w);
-                            }
-                        }
-                    }
-                    const float sub = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32_nowait(ts + c * 32, v[c & 1]);
-                        tmem_ld_wait();
+                    // Most rows see a whole tile or, when it is in the list for another row of
+                    // the group, nothing of it: then a row is on or off, and no element is looked
+                    // at alone.  An off row's elements become 2^-200 = 0.
+                    const bool full = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu, none = (mw[0] | mw[1] | mw[2] | mw[3]) == 0u;
+                    const bool whole_rows = __all_sync(0xffffffffu, full || none);
+                    if (__all_sync(0xffffffffu, none || !live)) {
+                        // no row of the warp sees the tile: P is zero
                         uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a = ex2_approx(fmaf(__uint_as_float(v[c & 1][i]), c2, -sub));
-                            float d = ex2_approx(fmaf(__uint_as_float(v[c & 1][i + 1]), c2, -sub));
-                            if (!all_full) {
-                                if (!((mw[c] >> i) & 1u)) a = 0.f;
-                                if (!((mw[c] >> (i + 1)) & 1u)) d = 0.f;
-                            }
-                            sum[(i >> 1) & 3] += a + d;
-                            w[i >> 1] = FP4 ? pack_f16(a, d) : pack_bf16(a, d);
-                        }
-                        tmem_st16(ts + c * 16, w);
+                        for (int i = 0; i < 16; ++i) w[i] = 0u;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_st16(ts + c * 16, w);
+                        tmem_st_wait();
+                    } else if (whole_rows) {
+                        softmax_tile<D, FP4, false>(ts, to, mw, full, j < 2, c2, m, l);
+                    } else {
+                        softmax_tile<D, FP4, true>(ts, to, mw, full, j < 2, c2, m, l);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st_wait();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfull + set);
+                if (j + 2 < sg.n) look(j + 2);
             }
             if (!ok) break;
             vbase += sg.n;

@@ -25,29 +25,40 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// mbar_wait for pipelines whose waits are mostly short: the timer that bounds
-// the wait is read only once 64 polls have failed, since a read takes longer
-// than such a wait.
-__device__ __forceinline__ bool ba_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const uint32_t a = smem_addr(bar);
-    uint64_t t0 = 0;
+// The whole warp waits on a barrier (bounded); all lanes learn the outcome.
+// A barrier that is through already costs one poll and a vote.  The rest is
+// out of line, for the kernels wait in some twenty places and run partly cold;
+// there lane 0 polls, and reads the timer that bounds the wait only once 64
+// polls have failed, since a read takes longer than most of these waits.
+static __device__ __noinline__ bool ba_wait_slow(uint32_t a, uint32_t parity, volatile int* abort_flag) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(a, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (abort_flag && *abort_flag) return false;
+        for (uint32_t it = 1; !mbar_try_wait(a, parity); ++it) {
+            if ((it & 63u) != 0) continue;
+            if (abort_flag && *abort_flag) {
+                ok = false;
+                break;
+            }
             const uint64_t t = global_ns();
-            if (t0 == 0) t0 = t;
-            else if (t - t0 > kWaitLimitNs) return false;
+            if (t0 == 0) {
+                t0 = t;
+            } else if (t - t0 > kWaitLimitNs) {
+                ok = false;
+                break;
+            }
         }
     }
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
-// Lane 0 waits; the warp learns the outcome.
 __device__ __forceinline__ bool warp_wait_b(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = ba_wait(bar, parity, abort_flag);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    const uint32_t a = smem_addr(bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    const bool ok = ba_wait_slow(a, parity, abort_flag);
+    // every lane has seen the phase, so that what came before it is visible to each
+    if (ok) mbar_try_wait(a, parity);
     __syncwarp();
     return ok;
 }

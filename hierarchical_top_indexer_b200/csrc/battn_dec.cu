@@ -509,7 +509,10 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
                 sees = e < np && r - s * p.PB < (list[min(e, np - 1)].x & 255);
                 const uint32_t rs = it % kRaw, slot = it % kS;
                 if (!(ok = warp_wait_b(rfull + rs, (it / kRaw) & 1, abort_flag))) break;
-                if (it >= kS && !(ok = warp_wait_b(empty + slot, (it / kS - 1) & 1, abort_flag))) break;
+                // the slot's last reader, P V of tile it - kS (this team saw the one before it - kS + 1
+                // through when it took its last tile, so the parity is that phase's)
+                const uint32_t last = it - kS;
+                if (it >= kS && !(ok = warp_wait_b(pempty + last % kBufs, (last / kBufs) & 1, abort_flag))) break;
                 const uint8_t* raw = smem + L::raw0 + rs * L::raw;
                 uint8_t* dst = smem + L::ring + slot * L::tile;
 #pragma unroll
@@ -621,14 +624,13 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
                 }
             }
         }
-        if (!ok && lane == 0) {
+        if (!ok) {
             // the copies in flight land before the CTA gives up its shared memory
-            volatile int keep_waiting = 0;
             *abort_flag = 1;
             constexpr uint32_t n = FP4 ? kRaw : kS;
-            if (!FP4 && seg > 0) ba_wait(qfull, (seg - 1) & 1, &keep_waiting);
+            if (!FP4 && seg > 0) warp_wait_b(qfull, (seg - 1) & 1, nullptr);
             for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
-                ba_wait((FP4 ? rfull : i & 1 ? vland : kland) + i % n, (i / (FP4 ? n : 6)) & 1, &keep_waiting);
+                warp_wait_b((FP4 ? rfull : i & 1 ? vland : kland) + i % n, (i / (FP4 ? n : 6)) & 1, nullptr);
         }
     } else if (warp == L::warp_s) {
         // ------------------------------------------------------- S = K Q^T
@@ -645,8 +647,9 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
                 else ok = warp_wait_b(kland + slot, (2 * it / 6) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t td = uni(tm + L::tmem_s + sb * kBdN);
-                const uint32_t a = uni(FP4 ? tm + L::tmem_k + sb * (D / 2) : k_lo + slot * (L::tile >> 4));
+                const uint32_t at = uni(slot * kSB + sb);
+                const uint32_t td = tm + L::tmem_s + (at % kSB) * kBdN;
+                const uint32_t a = FP4 ? tm + L::tmem_k + (at % kSB) * (D / 2) : k_lo + (at / kSB) * (L::tile >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
@@ -686,13 +689,14 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
                 if (!FP4) ok = ok && warp_wait_b(vland + slot, (n / 6) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t td = uni(tm + L::tmem_o + set * kBdN), a = uni(v_lo + slot * (L::tile >> 4));
-                const uint32_t b = uni(p_lo + buf * (kBdN * 256 >> 4)), more = uni(j >= kSets ? 1u : 0u);
+                const uint32_t at = uni(slot * 8 + buf * 2 + (j >= kSets ? 1 : 0));   // buf's set: buf % kSets
+                const uint32_t td = tm + L::tmem_o + ((at >> 1) % kSets) * kBdN, a = v_lo + (at >> 3) * (L::tile >> 4);
+                const uint32_t b = p_lo + ((at >> 1) & 3) * (kBdN * 256 >> 4), more = at & 1;
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
                         umma_bf16(td, desc64(a + s * (2048 >> 4), kHi128), desc64(b + s * (512 >> 4), kHiP), id, s > 0 ? 1u : more);
-                    umma_commit(empty + slot);
+                    if (!FP4) umma_commit(empty + slot);
                     umma_commit(pempty + buf);
                     if (j + 1 == sg.n) umma_commit(odone + (seg & 1));
                 }
@@ -702,10 +706,9 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         }
         if (!ok) *abort_flag = 1;
         // every MMA done before TMEM is freed (a bounded wait that an abort does not cut short)
-        volatile int keep_waiting = 0;
         if (elect_one()) umma_commit(done);
         __syncwarp();
-        if (!warp_wait_b(done, 0, &keep_waiting)) ok = false;
+        if (!warp_wait_b(done, 0, nullptr)) ok = false;
         __syncwarp();
     }
     if (!ok && lane == 0) {
