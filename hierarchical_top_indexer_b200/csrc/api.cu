@@ -802,7 +802,7 @@ int check_cache_rows(const hisa_attn_kv* c, const void* K, const void* V, const 
     if (n == 0) return HISA_OK;
     if (!K || !V || !seq || !aligned(K, 16) || !aligned(V, 16) || !aligned(seq, 4) || (pos && !aligned(pos, 4)))
         return HISA_E_INVAL;
-    if (static_cast<long long>(n) * c->heads * (c->d / 16) > INT_MAX * 256ll) return HISA_E_UNSUPPORTED;
+    if (static_cast<long long>(n) * c->heads > INT_MAX) return HISA_E_UNSUPPORTED;
     return HISA_OK;
 }
 

@@ -78,17 +78,15 @@ template <bool FP4>
 __global__ void __launch_bounds__(kCacheThreads) cache_store_kernel(const CacheParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int groups = p.d >> 4;
-    const long long k = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-    const int per_tok = p.heads * groups;
-    if (k >= static_cast<long long>(p.n) * per_tok) return;
-    const int i = static_cast<int>(k / per_tok);
-    const int hg = static_cast<int>(k - static_cast<long long>(i) * per_tok);
-    const int h = hg / groups, g = hg - h * groups;
+    const int lg = p.d == 128 ? 3 : 2, groups = 1 << lg;
+    const size_t k = static_cast<size_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+    const uint32_t ih = static_cast<uint32_t>(k >> lg), g = static_cast<uint32_t>(k) & (groups - 1);
+    if (ih >= static_cast<uint32_t>(p.n) * p.heads) return;
+    const int i = ih / static_cast<uint32_t>(p.heads), h = ih - i * p.heads;
     const bool val = blockIdx.y != 0;
-    const long long row = cache_row(p, i, h, hg == 0 && !val);
+    const long long row = cache_row(p, i, h, h == 0 && g == 0 && !val);
     if (row < 0) return;
-    const uint4* src = reinterpret_cast<const uint4*>((val ? p.v_rows : p.k_rows) + static_cast<size_t>(k) * 16);
+    const uint4* src = reinterpret_cast<const uint4*>((val ? p.v_rows : p.k_rows) + k * 16);
     const uint4 a = __ldcs(src), b = __ldcs(src + 1);
     uint8_t* dst = static_cast<uint8_t*>(val ? p.v : p.k);
     if (!FP4) {
@@ -114,16 +112,14 @@ template <bool FP4>
 __global__ void __launch_bounds__(kCacheThreads) cache_load_kernel(const CacheParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int groups = p.d >> 4;
-    const long long k = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-    const int per_tok = p.heads * groups;
-    if (k >= static_cast<long long>(p.n) * per_tok) return;
-    const int i = static_cast<int>(k / per_tok);
-    const int hg = static_cast<int>(k - static_cast<long long>(i) * per_tok);
-    const int h = hg / groups, g = hg - h * groups;
+    const int lg = p.d == 128 ? 3 : 2, groups = 1 << lg;
+    const size_t k = static_cast<size_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+    const uint32_t ih = static_cast<uint32_t>(k >> lg), g = static_cast<uint32_t>(k) & (groups - 1);
+    if (ih >= static_cast<uint32_t>(p.n) * p.heads) return;
+    const int i = ih / static_cast<uint32_t>(p.heads), h = ih - i * p.heads;
     const bool val = blockIdx.y != 0;
-    const long long row = cache_row(p, i, h, hg == 0 && !val);
-    uint4* out = reinterpret_cast<uint4*>((val ? p.v_out : p.k_out) + static_cast<size_t>(k) * 16);
+    const long long row = cache_row(p, i, h, h == 0 && g == 0 && !val);
+    uint4* out = reinterpret_cast<uint4*>((val ? p.v_out : p.k_out) + k * 16);
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (row >= 0) {
         const uint8_t* src = static_cast<const uint8_t*>(val ? p.v : p.k);

@@ -224,6 +224,7 @@ struct RopeParams {
     int interleaved, transpose;
     float gain;
     int tasks, rows_blk, heads_blk;      // set by launch_rope
+    uint32_t tasks_inv, heads_inv;
     uint64_t turns[HISA_ROPE_MAX_PAIRS]; // turns per position of each pair, 64-bit fixed point
 };
 cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s);

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTasks = 4;          // per thread
-constexpr int kRopeMaxSc = 4096;       // (row, pair) sine and cosine entries per block
+constexpr int kRopeMaxSc = 1024;       // (row, pair) sine and cosine entries per block
 
 // Sine and cosine (times gain) of pair i at position pos.
 __device__ __forceinline__ float2 rope_sc(const RopeParams& p, int pos, int i) {
@@ -55,7 +55,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     const int np = p.rot >> 1;
     const int pair_tasks = MODE == 0 ? p.rot >> 4 : 0;
     const int th = p.tasks;   // per (row, head)
-    const int total = nr * nh * th;
     const bool in_place = p.x == p.y;
     uint4 va[kRopeTasks], vb[kRopeTasks];
     size_t oa[kRopeTasks];
@@ -65,10 +64,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     for (int u = 0; u < kRopeTasks; ++u) {
         const int k = u * kRopeThreads + threadIdx.x;
         rel[u] = -2;
-        if (k >= total) continue;
-        const int t = k % th, hr = k / th;
-        const int h = hr % nh;
-        rr[u] = hr / nh;
+        // k = (row * heads_blk + head) * tasks + task, every factor below 2^10
+        const int hr = static_cast<uint32_t>(k) * p.tasks_inv >> 20, t = k - hr * th;
+        rr[u] = static_cast<uint32_t>(hr) * p.heads_inv >> 20;
+        const int h = hr - rr[u] * p.heads_blk;
+        if (rr[u] >= nr || h >= nh) continue;
         const size_t base = (static_cast<size_t>(row0 + rr[u]) * p.heads + h0 + h) * p.d;
         if (MODE == 0) {
             int e = p.off + 8 * t;
@@ -191,6 +191,8 @@ cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s) {
         p.rows_blk = static_cast<int>(want / per_row);
         if (p.rows_blk > most) p.rows_blk = most;
     }
+    p.tasks_inv = (1u << 20) / p.tasks + 1;    // x * inv >> 20 = x / tasks for x, tasks below 2^10
+    p.heads_inv = (1u << 20) / p.heads_blk + 1;
     cfg.gridDim = dim3(static_cast<unsigned>((p.rows + p.rows_blk - 1) / p.rows_blk),
                        static_cast<unsigned>((p.heads + p.heads_blk - 1) / p.heads_blk));
     return half_vec ? cudaLaunchKernelEx(&cfg, rope_vec_kernel<0>, p) : cudaLaunchKernelEx(&cfg, rope_vec_kernel<1>, p);
