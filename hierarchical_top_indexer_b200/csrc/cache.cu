@@ -13,8 +13,9 @@
 // break a tie.
 //
 // Bound: 2 bytes read and 0.5625 written per element (store; load the other
-// way).  One thread per group: two 16-byte loads, one 8-byte store of codes
-// and one byte of scale; the groups of a row are neighbouring threads.
+// way).  One thread per group of the keys and the same of the values: four
+// 16-byte loads in flight before it knows its row, two 8-byte stores of codes
+// and two bytes of scale; the groups of a row are neighbouring threads.
 #include "hisa_kernels.cuh"
 
 namespace hisa {
@@ -73,7 +74,37 @@ __device__ __forceinline__ uint32_t codes8(uint32_t w0, uint32_t w1, uint32_t w2
     return r;
 }
 
-// Thread (token, head, group of 16 elements); blockIdx.y 0: keys, 1: values.
+// One row's group of 16 elements in 4 bits.
+__device__ __forceinline__ void store_fp4(const uint4& a, const uint4& b, float mul, uint8_t* codes, uint8_t* scale) {
+    const float want = __fdiv_rn(max_abs16(a, b), 6.f * mul);
+    const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+    const float s = __half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)) * mul;
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    uint2 c;
+    c.x = codes8(a.x, a.y, a.z, a.w, inv);
+    c.y = codes8(b.x, b.y, b.z, b.w, inv);
+    *reinterpret_cast<uint2*>(codes) = c;
+    *scale = s8;
+}
+
+__device__ __forceinline__ void load_fp4(const uint2& c, uint8_t scale, float mul, uint4* out) {
+    const float s = __half2float(__nv_cvt_fp8_to_halfraw(scale, __NV_E4M3)) * mul;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t f[4];
+        e2m1x8_to_f16(j ? c.y : c.x, f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[q]));
+            w[4 * j + q] = pack_bf16(v.x * s, v.y * s);   // exact
+        }
+    }
+    __stcs(out, make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(out + 1, make_uint4(w[4], w[5], w[6], w[7]));
+}
+
+// Thread (token, head, group of 16 elements), keys and values.
 template <bool FP4>
 __global__ void __launch_bounds__(kCacheThreads) cache_store_kernel(const CacheParams p) {
     grid_dependency_wait();
@@ -82,29 +113,24 @@ __global__ void __launch_bounds__(kCacheThreads) cache_store_kernel(const CacheP
     const size_t k = static_cast<size_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
     const uint32_t ih = static_cast<uint32_t>(k >> lg), g = static_cast<uint32_t>(k) & (groups - 1);
     if (ih >= static_cast<uint32_t>(p.n) * p.heads) return;
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k_rows + k * 16);
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v_rows + k * 16);
+    const uint4 ka = __ldcs(ks), kb = __ldcs(ks + 1), va = __ldcs(vs), vb = __ldcs(vs + 1);
     const int i = ih / static_cast<uint32_t>(p.heads), h = ih - i * p.heads;
-    const bool val = blockIdx.y != 0;
-    const long long row = cache_row(p, i, h, h == 0 && g == 0 && !val);
+    const long long row = cache_row(p, i, h, h == 0 && g == 0);
     if (row < 0) return;
-    const uint4* src = reinterpret_cast<const uint4*>((val ? p.v_rows : p.k_rows) + k * 16);
-    const uint4 a = __ldcs(src), b = __ldcs(src + 1);
-    uint8_t* dst = static_cast<uint8_t*>(val ? p.v : p.k);
-    if (!FP4) {
-        uint4* o = reinterpret_cast<uint4*>(dst + (static_cast<size_t>(row) * p.d + 16 * g) * 2);
-        o[0] = a;
-        o[1] = b;
-        return;
+    const size_t at = (static_cast<size_t>(row) << lg) + g;   // group of the cache
+    if (FP4) {
+        store_fp4(ka, kb, p.k_mul, static_cast<uint8_t*>(p.k) + 8 * at, p.k_scale + at);
+        store_fp4(va, vb, p.v_mul, static_cast<uint8_t*>(p.v) + 8 * at, p.v_scale + at);
+    } else {
+        uint4* ko = reinterpret_cast<uint4*>(p.k) + 2 * at;
+        uint4* vo = reinterpret_cast<uint4*>(p.v) + 2 * at;
+        ko[0] = ka;
+        ko[1] = kb;
+        vo[0] = va;
+        vo[1] = vb;
     }
-    const float mul = val ? p.v_mul : p.k_mul;
-    const float want = __fdiv_rn(max_abs16(a, b), 6.f * mul);
-    const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-    const float s = __half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)) * mul;
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint2 c;
-    c.x = codes8(a.x, a.y, a.z, a.w, inv);
-    c.y = codes8(b.x, b.y, b.z, b.w, inv);
-    *reinterpret_cast<uint2*>(dst + static_cast<size_t>(row) * (p.d >> 1) + 8 * g) = c;
-    (val ? p.v_scale : p.k_scale)[static_cast<size_t>(row) * groups + g] = s8;
 }
 
 // The way back: rows [n, heads, d] bf16 (zero rows where the name is bad).
@@ -117,37 +143,29 @@ __global__ void __launch_bounds__(kCacheThreads) cache_load_kernel(const CachePa
     const uint32_t ih = static_cast<uint32_t>(k >> lg), g = static_cast<uint32_t>(k) & (groups - 1);
     if (ih >= static_cast<uint32_t>(p.n) * p.heads) return;
     const int i = ih / static_cast<uint32_t>(p.heads), h = ih - i * p.heads;
-    const bool val = blockIdx.y != 0;
-    const long long row = cache_row(p, i, h, h == 0 && g == 0 && !val);
-    uint4* out = reinterpret_cast<uint4*>((val ? p.v_out : p.k_out) + k * 16);
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (row >= 0) {
-        const uint8_t* src = static_cast<const uint8_t*>(val ? p.v : p.k);
-        if (!FP4) {
-            const uint4* r = reinterpret_cast<const uint4*>(src + (static_cast<size_t>(row) * p.d + 16 * g) * 2);
-            a = r[0];
-            b = r[1];
-        } else {
-            const uint2 c = *reinterpret_cast<const uint2*>(src + static_cast<size_t>(row) * (p.d >> 1) + 8 * g);
-            const uint8_t s8 = (val ? p.v_scale : p.k_scale)[static_cast<size_t>(row) * groups + g];
-            const float s = __half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)) * (val ? p.v_mul : p.k_mul);
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t f[4];
-                e2m1x8_to_f16(j ? c.y : c.x, f);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[q]));
-                    w[4 * j + q] = pack_bf16(v.x * s, v.y * s);   // exact
-                }
-            }
-            a = make_uint4(w[0], w[1], w[2], w[3]);
-            b = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+    const long long row = cache_row(p, i, h, h == 0 && g == 0);
+    uint4* ko = reinterpret_cast<uint4*>(p.k_out + k * 16);
+    uint4* vo = reinterpret_cast<uint4*>(p.v_out + k * 16);
+    if (row < 0) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        ko[0] = ko[1] = vo[0] = vo[1] = z;
+        return;
     }
-    __stcs(out, a);
-    __stcs(out + 1, b);
+    const size_t at = (static_cast<size_t>(row) << lg) + g;
+    if (FP4) {
+        const uint2 kc = *(reinterpret_cast<const uint2*>(p.k) + at), vc = *(reinterpret_cast<const uint2*>(p.v) + at);
+        const uint8_t k8 = p.k_scale[at], v8 = p.v_scale[at];
+        load_fp4(kc, k8, p.k_mul, ko);
+        load_fp4(vc, v8, p.v_mul, vo);
+    } else {
+        const uint4* kr = reinterpret_cast<const uint4*>(p.k) + 2 * at;
+        const uint4* vr = reinterpret_cast<const uint4*>(p.v) + 2 * at;
+        const uint4 ka = kr[0], kb = kr[1], va = vr[0], vb = vr[1];
+        __stcs(ko, ka);
+        __stcs(ko + 1, kb);
+        __stcs(vo, va);
+        __stcs(vo + 1, vb);
+    }
 }
 
 template <typename K>
@@ -157,7 +175,7 @@ cudaError_t launch_rows(K kernel, const CacheParams& p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((threads + kCacheThreads - 1) / kCacheThreads), 2);
+    cfg.gridDim = dim3(static_cast<unsigned>((threads + kCacheThreads - 1) / kCacheThreads));
     cfg.blockDim = dim3(kCacheThreads);
     cfg.stream = s;
     cfg.attrs = attr;
