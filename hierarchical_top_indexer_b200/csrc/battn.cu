@@ -726,75 +726,78 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
 
 // The groups that no single segment covered.  Group x = (key head, group) is
 // tiles [a, a + T) of all; the CTA whose run holds tile y is
-// ((y + 1) * n - 1) / all with n CTAs at work, the first of them left its part in its slot 1,
-// the others in their slots 0.  One warp per MMA row; also the zero output of
-// groups without a tile.
-template <int D>
+// ((y + 1) * n - 1) / all with n CTAs at work, the first of them left its part
+// in its slot 1, the others in their slots 0.  W warps take every W-th part of
+// an MMA row (8 where few rows are split over many CTAs, whose parts one warp
+// would fetch one after another: 63 parts of 4 KB took 24 us; else 1), and
+// their sums are added in a fixed order.  Also the zero output of groups
+// without a tile.
+template <int D, int W>
 __global__ void __launch_bounds__(256) join_kernel(const BattnParams p, int grid) {
+    __shared__ float s_acc[W > 1 ? W : 1][D];
+    __shared__ float s_sum[W];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int x = blockIdx.x;
     const int h = x / p.groups, g = x - h * p.groups;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int r = W > 1 ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) * 8 + warp;
     const int rr = r / p.G, row = g * p.R + rr;
     if (rr >= p.R || row >= p.n_q) return;
-    const int t0 = p.tile0[g], T = p.tile0[g + 1] - t0;
-    const long long tot = p.tile0[p.groups], all = tot * p.Hkv;
+    const int t0 = __ldcg(p.tile0 + g), T = __ldcg(p.tile0 + g + 1) - t0;
+    const long long tot = __ldcg(p.tile0 + p.groups), all = tot * p.Hkv;
     const size_t orow = static_cast<size_t>(row) * p.Hq + h * p.G + (r - rr * p.G);
     constexpr int E = D / 32;   // elements per lane
     float acc[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    float M = -INFINITY, Ls = 0.f;
+    float M = -INFINITY, sum = 0.f;
     if (T > 0) {
-        const long long a = h * tot + t0;
-        const long long n = min(static_cast<long long>(grid), all);
+        const long long a = h * tot + t0, n = min(static_cast<long long>(grid), all);
         const int c0 = static_cast<int>(((a + 1) * n - 1) / all), c1 = static_cast<int>(((a + T) * n - 1) / all);
         if (c0 == c1) return;   // finished in place
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const int slot = 2 * c + (c == c0 ? 1 : 0);
-            M = fmaxf(M, p.part_ml[slot * p.prow + r].x);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int cb = c0; cb <= c1; cb += 32) {
-            const int c = cb + lane;
-            float w = 0.f;
-            if (c <= c1) {
-                const float2 v = p.part_ml[(2 * c + (c == c0 ? 1 : 0)) * p.prow + r];
-                w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-                Ls += w * v.y;
-            }
-            const int some = min(32, c1 - cb + 1);
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.part_ml + (2 * c + (c == c0 ? 1 : 0)) * p.prow + r).x);
+        M = warp_max(M);
 #pragma unroll 4
-            for (int k = 0; k < some; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                const int ck = cb + k;
-                const float* po = p.part_o + (static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * p.prow + r) * D + lane * E;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(po);
-                    acc[0] += wk * v.x;
-                    acc[1] += wk * v.y;
-                    acc[E - 2] += wk * v.z;
-                    acc[E - 1] += wk * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(po);
-                    acc[0] += wk * v.x;
-                    acc[1] += wk * v.y;
-                }
+        for (int c = c0 + (W > 1 ? warp : 0); c <= c1; c += W) {
+            const size_t part = static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.prow + r;
+            const float2 v = __ldcg(p.part_ml + part);
+            const float w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+            sum += w * v.y;
+            const float* po = p.part_o + part * D + lane * E;
+            if (E == 4) {
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(po));
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
+                acc[E - 2] += w * o.z;
+                acc[E - 1] += w * o.w;
+            } else {
+                const float2 o = __ldcg(reinterpret_cast<const float2*>(po));
+                acc[0] += w * o.x;
+                acc[1] += w * o.y;
             }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
     }
-    const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
+    if (W > 1) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) s_acc[warp][lane * E + i] = acc[i];
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] += s_acc[w][lane * E + i];
+            sum += s_sum[w];
+        }
+    }
+    const float inv = sum > 0.f ? p.out_mul / sum : 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] *= inv;
     uint32_t* out = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * E);
     out[0] = pack_bf16(acc[0], acc[1]);
     if (E == 4) out[1] = pack_bf16(acc[E - 2], acc[E - 1]);
-    if (lane == 0 && p.lse) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[orow] = sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -829,10 +832,12 @@ cudaError_t launch_typed(const CUtensorMap& qm, const CUtensorMap& km, const CUt
         e = cudaLaunchKernelEx(&cfg, battn_kernel<D, FP4>, qm, km, vm, p);
     }
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * p.Hkv, static_cast<unsigned>((p.R * p.G + 7) / 8));
+    const unsigned items = static_cast<unsigned>(p.groups) * p.Hkv;
+    const bool spread = 8 * items <= static_cast<unsigned>(grid);   // eight parts or more to a (key head, group)
+    cfg.gridDim = dim3(items, static_cast<unsigned>(spread ? p.R * p.G : (p.R * p.G + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, grid);
+    return spread ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, p, grid) : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p, grid);
 }
 
 }  // namespace

@@ -97,6 +97,12 @@ constexpr uint32_t kHi128 = desc_hi(1024, 2);   // both majors, 128-byte swizzle
 
 __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
 
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // A run's place: key head h, group g, tiles [t0, t0 + n) of the group's T.
 struct BaSeg {
     int h, g, t0, n, T;

@@ -78,12 +78,6 @@ __host__ __device__ constexpr uint32_t idesc_bd(bool f16, bool a_mn_major, bool 
 // other group of four tokens; 8-token groups 256 B apart.
 constexpr uint32_t kHiP = desc_hi(256, 6);
 
-__device__ __forceinline__ float warp_max(float x) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // 16-byte chunk c of code row r, as the swizzled TMA load placed it.
 template <int D>
 __device__ __forceinline__ int code_chunk(int r, int c) {
