@@ -1484,6 +1484,7 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
     p.k_scale = c->k_scale;
     p.v_scale = c->v_scale;
     p.scale_log2 = scale * 1.4426950408889634f * (fp4 ? c->k_mul : 1.f);
+    if (!(p.scale_log2 > 0.f) || !std::isfinite(p.scale_log2)) return HISA_E_INVAL;   // scale * k_mul out of fp32's range
     p.out_mul = fp4 ? c->v_mul : 1.f;
     p.out = out;
     p.lse = lse;

@@ -8,7 +8,7 @@
 //     out = sum_s softmax(z)_s V[s],   lse = log sum_s exp z_s.
 //
 // Plan.  R consecutive rows form a group whose (row, head) pairs fill the 128
-// rows of one MMA: R = 128 / G where rows share sequences (a chunk), else 1.
+// rows of one MMA: R = 128 / G for a chunk (battn_layout has the rule), else 1.
 // A group reads the union of its rows' blocks once, each row masking what it
 // did not keep: neighbouring rows keep much the same blocks, and a tile of
 // keys then serves up to 128 (row, head) pairs instead of G.  plan_kernel
@@ -843,11 +843,19 @@ cudaError_t launch_typed(const CUtensorMap& qm, const CUtensorMap& km, const CUt
 }  // namespace
 
 size_t battn_layout(BattnParams& p, void* ws) {
-    // rows share their keys where there are more rows than sequences (a chunk)
+    // Groups of rows where there are more rows than sequences.  Over whole prefixes a group
+    // reads what each of its rows would (8 sequences of 32K keys, G = 8: 2 rows each 83 us in
+    // groups, 93 us alone; 4 rows 78 and 159 us).  Over kept blocks it reads their union, which
+    // pays with some rows to a group and some groups (64 kept of 256 blocks, G = 8, R = 16: 64
+    // rows of one sequence 62 us in groups, 54 us alone; 128 rows 79 and 87 us; 4096 rows 676
+    // and 2105 us; 9 rows of 8 sequences 86 and 62 us, 32 rows of 8 104 and 166 us), and where
+    // the kernel for lone rows does not serve (64 rows of G = 32: 72 and 92 us).
     p.G = p.Hq / p.Hkv;
-    p.R = p.n_q > p.batch ? 128 / p.G : 1;
-    p.groups = (p.n_q + p.R - 1) / p.R;
     const bool sparse = p.mb > 0;
+    const int most = 128 / p.G;
+    const bool many = p.n_q >= 96 && p.n_q >= 2ll * most * p.batch;
+    p.R = p.n_q > p.batch && (!sparse || p.G > kBattnDecHeads || many) ? most : 1;
+    p.groups = (p.n_q + p.R - 1) / p.R;
     p.PB = sparse && p.B < 128 ? p.B : 128;
     p.S = 128 / p.PB;
     p.ppb = sparse && p.B > 128 ? p.B / 128 : 1;
@@ -871,7 +879,9 @@ size_t battn_layout(BattnParams& p, void* ws) {
     p.tiles = reinterpret_cast<int*>(take(static_cast<size_t>(p.groups) * 4));
     p.tile0 = reinterpret_cast<int*>(take(static_cast<size_t>(p.groups + 1) * 4));
     p.bits = reinterpret_cast<uint32_t*>(take(p.R > 1 ? static_cast<size_t>(p.n_q) * p.W * 4 : 0));
-    // a lone row with few heads: tokens in the MMA's rows, two CTAs per SM
+    // A lone row with few heads: tokens in the MMA's rows (64 rows of 8192 kept keys, G = 8:
+    // 344 us, and 352 us in the 128-row kernel; G = 16: 104 and 110 us; 16 whole prefixes of
+    // 64K 4-bit keys, G = 16: 101 and 187 us)
     p.dec = p.R == 1 && p.G <= kBattnDecHeads;
     p.prow = p.dec ? kBattnDecHeads : 128;
     const size_t parts = static_cast<size_t>(2) * kBattnMaxSms * (p.dec ? 2 : 1) * p.prow;

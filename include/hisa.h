@@ -452,7 +452,8 @@ int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, do
 
 /*
  * hisa_rope — y = the rotated rows of x.
- *   x, y   [rows, heads, d] bf16; y may be x (in place) but not overlap it otherwise
+ *   x, y   [rows, heads, d] bf16, heads in 1..65536; y may be x (in place) but
+ *          not overlap it otherwise
  *   pos    [rows] int32: the position of each row (hisa_kv.len before an
  *          append names the position of the token about to be appended)
  *   transpose  0, or 1 for the transposed map (t negated): the gradient of the
@@ -540,7 +541,8 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  *   ws     workspace of at least hisa_block_attn_workspace_bytes(...) bytes
  * A row that sees no token gives out = 0 and lse = -inf; a row whose position
  * is not inside its prefix does too, and sets HISA_DEV_BAD_QUERY.  Sizes: B as
- * hisa_select, at most 2^20 blocks per sequence, G in 1..128.
+ * hisa_select, at most 2^20 blocks per sequence, G in 1..128, scale positive
+ * and, times k_mul, in fp32's range.
  * Numerics: logits from exact products (bf16, or f16 for FP4 rows) summed in
  * fp32; softmax maxima and sums in fp32; the weights are rounded to bf16 (f16
  * for FP4 rows) for the product with the values, accumulated in fp32; out is

@@ -247,12 +247,29 @@ def test_chunks(dtype, d, Hkv, G, B, m):
 
 
 @DTYPES
+@pytest.mark.parametrize("d,Hkv,G", [(128, 2, 8), (64, 1, 3), (64, 1, 1), (128, 1, 32)])
+@pytest.mark.parametrize("B,m", [(128, 3), (64, 6), (16, 9), (384, 1)])
+def test_chunks_of_many_rows(dtype, d, Hkv, G, B, m):
+    """Enough rows for groups over kept blocks: the union of a group's lists, each row masking what it did not keep."""
+    n = max(100, 4 * (128 // G) + 3)
+    rng = np.random.default_rng(n + B)
+    q_seq = np.sort(rng.integers(0, 2, n))
+    q_pos = np.where(q_seq == 0, 640, 300) - rng.integers(0, 300, n)
+    q_pos[5], q_pos[6], q_seq[7] = -1, 641, 9
+    c = Case(dtype, d, Hkv, G, 656, [641, 301], q_seq, q_pos, B, m, seed=B + G)
+    near = rng.random(n) < 0.7                          # neighbours keep much the same blocks, some a list of their own
+    c.blocks[near] = c.blocks[0]
+    c.blocks[20:30] = -1
+    c.check(*c.call())
+
+
+@DTYPES
 def test_rows_of_many_sequences_in_one_group(dtype):
     """Rows in no order of sequences: a group's tiles mix pieces of several."""
     rng = np.random.default_rng(5)
     lens = [40, 1, 130, 0, 64, 17, 99]
-    q_seq = rng.integers(0, 7, 50)
-    q_pos = np.maximum(np.asarray(lens)[q_seq] - 1 - rng.integers(0, 3, 50), 0)
+    q_seq = rng.integers(0, 7, 460)
+    q_pos = np.maximum(np.asarray(lens)[q_seq] - 1 - rng.integers(0, 3, 460), 0)
     for B, m in ((128, 0), (16, 4), (8, 9)):
         c = Case(dtype, 64, 1, 4, 144, lens, q_seq, q_pos, B, m, seed=B)
         c.check(*c.call())
@@ -342,14 +359,103 @@ def test_given_buffers_streams_and_graphs(dtype):
     assert (guard[n] == 5).all()                        # rows behind the last stay
 
 
+@DTYPES
+def test_rows_of_one_sequence_alone(dtype):
+    """No more rows than sequences, yet several of one sequence: each row alone."""
+    c = Case(dtype, 128, 2, 4, 640, [640, 500, 1], [0, 0, 0], [639, 100, 0], 64, 5, seed=8)
+    c.check(*c.call())
+
+
+@DTYPES
+def test_two_calls_at_once(dtype):
+    """Two streams, a workspace each, on one cache; then both replayed as graphs that share a workspace in turn."""
+    one = Case(dtype, 128, 2, 8, 4096, [4096, 3000], [0, 1], [4095, 2999], 64, 20, seed=12)
+    two = Case(dtype, 128, 2, 8, 4096, [4096, 3000], np.repeat([0, 1], 100), np.r_[3900:4000, 2900:3000], 64, 20, seed=12)
+    two.c, two.K, two.V = one.c, one.K, one.V
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(10):
+        outs = [x.call(stream=s) for x, s in zip((one, two), streams)]
+    torch.cuda.synchronize()
+    for x, (out, lse) in zip((one, two), outs):
+        x.check(out, lse)
+    size = lambda x: hisa.hisa_block_attn_workspace_bytes(x.c, x.Q.shape[0], 16, 64, 20)  # noqa: E731
+    ws = hisa.workspace(max(size(one), size(two)))
+    args = [(x, _i32(x.q_seq), _i32(x.q_pos), _i32(x.blocks)) for x in (one, two)]
+    graphs, got = [], []
+    for x, seq, pos, blk in args:
+        run = lambda: hisa.hisa_block_attn(x.c, x.Q, seq, pos, blk, B=64, scale=x.scale, ws=ws)  # noqa: E731,B023
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(run())
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (out, lse), (o2, l2) in zip(outs, got):
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype,d,cap,B", [("bf16", 128, 9_000_000, 128), ("fp4", 128, 34_000_000, 256), ("bf16", 64, 1 << 23, 8)])
+def test_offsets_past_32_bits(dtype, d, cap, B):
+    """Rows whose bytes lie past 2^31 from the cache's start (and 2^20 blocks in a sequence): stored, read back, attended to."""
+    c = hisa.AttnCache(1, cap, 1, d, dtype, lens=_i32([cap]))
+    rng = np.random.default_rng(1)
+    last = (cap - 1) // B
+    blocks = np.array([[last, last - 2, 0, last // 2]])
+    tok = np.concatenate([np.arange(j * B, min((j + 1) * B, cap)) for j in blocks[0]])
+    K, V = (_bf(rng.standard_normal((len(tok), 1, d))) for _ in "kv")
+    seq = _i32(np.zeros(len(tok)))
+    hisa.hisa_cache_store(c, K, V, seq, _i32(tok))
+    k, v = hisa.hisa_cache_load(c, seq, _i32(tok))
+    Q = _bf(rng.standard_normal((1, 4, d)))
+    order = np.argsort(tok)
+    near = [np.array_equal(_f64(a), _f64(b) if dtype == "bf16" else ref.fp4_rows(_f64(b))[2]) for a, b in ((k, K), (v, V))]
+    assert all(near)
+    r = ref.block_attn(_f64(Q), _f64(k)[order].swapaxes(0, 1)[None], _f64(v)[order].swapaxes(0, 1)[None], [0], [len(tok) - 1], None, 1,
+                       1 / math.sqrt(d))
+    out, lse = hisa.hisa_block_attn(c, Q, _i32([0]), None, _i32(blocks), B=B)
+    ref.check_block_attn(_f64(out), _f64(lse), r, d, dtype == "fp4")
+    # 120 rows of one sequence: the other kernel
+    out, lse = hisa.hisa_block_attn(c, Q.repeat(120, 1, 1), _i32(np.zeros(120)), None, _i32(blocks.repeat(120, 0)), B=B)
+    r = {x: np.repeat(y, 120, 0) for x, y in r.items()}
+    ref.check_block_attn(_f64(out), _f64(lse), r, d, dtype == "fp4")
+    assert c.status_bits() == 0
+
+
+def test_scales_at_the_ends_of_their_range():
+    c = Case("fp4", 64, 1, 2, 64, [64], [0], [63], 128, 0, seed=2)
+    c.c._struct.k_mul = 2.0 ** 60
+    with pytest.raises(hisa.HisaError) as e:
+        hisa.hisa_block_attn(c.c, c.Q, _i32([0]), scale=1e30)
+    assert e.value.code == hisa.HISA_E_INVAL
+    c.c._struct.k_mul = 1.0
+    for scale in (1e-30, 1e-3, 40.0):
+        c.scale = scale
+        c.check(*c.call())
+    c = Case("fp4", 128, 1, 3, 256, [256], [0], [255], 128, 0, seed=2)
+    for size in (2.0 ** -120, 2.0 ** 100):               # queries far from 1, brought back by the scale
+        q = c.Q
+        c.Q, c.scale = (q.double() * size).to(torch.bfloat16), 1 / (math.sqrt(128) * size)
+        if size > 1 or c.scale < 3e38:
+            c.check(*c.call())
+        c.Q = q
+
+
 # --------------------------------------------------------------- together
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("m", [4, 100])
 @pytest.mark.parametrize("n_q", [4, 600])
-def test_select_blocks_is_stage_one(m, n_q):
+def test_select_blocks_is_stage_one(m, n_q, dtype):
     from hisa_inputs import make_case
     rng = np.random.default_rng(n_q)
-    case = make_case(batch=2, L=[4096, 3000], H=16, d=128, B=64, m=m, k=64, seed=3,
+    case = make_case(batch=2, L=[4096, 3000], H=16, d=128, B=64, m=m, k=64, seed=3, dtype=dtype,
                      positions=[np.sort(rng.integers(0, 4096, n_q // 2)), np.sort(rng.integers(0, 3000, n_q // 2))])
     kv = hisa.KVCache.from_case(case)
     hisa.hisa_pool_blocks(kv)
