@@ -37,6 +37,14 @@
 // P is rounded to bf16 (2^-8 relative) or f16 (2^-11); everything else is fp32.
 // f16 P is kept 2^7 larger, so that weights down to 2^-21 of the largest keep
 // all their bits and only those below 2^-32 of it vanish.
+//
+// Bound (d = 128): 4096 rows of one sequence, 64 of 256 blocks each, 16 heads
+// over 2 key heads, 676 us: about 2400 cycles a tile, of which the 2^x unit
+// takes 1024 and the MMAs 1024; the rest is the chain of each set (S, softmax,
+// P V), because P takes S's place and the next S of the set waits for P V.
+// 4-bit rows, 2 x 512 rows causal over 8191 keys, 32 heads over 4: 213 us.
+// An element-wise mask costs twice the whole tile, hence the rows that are on
+// or off; a single polling lane per wait cost twice the kernel (1459 us).
 #include "battn.cuh"
 
 namespace hisa {
