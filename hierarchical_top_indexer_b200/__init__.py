@@ -669,6 +669,14 @@ class _on:
             self._dev.__exit__(*exc)
 
 
+def _run(device, stream, call, *args):
+    """call(raw stream, *args) with `device` current and buffers made on `stream`."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(device.index), *args)
+    with _on(device, stream) as s:
+        return call(s, *args)
+
+
 def _want(fn: str, name: str, t, dtype, device, shape):
     """The library sees pointers only: a tensor of another type, device, shape
     or layout than the call reads is refused here.  -1 in shape: any size."""
@@ -743,15 +751,21 @@ def hisa_rope(plan: hisa_rope_plan, x: torch.Tensor, pos: torch.Tensor, out: Opt
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() not in (2, 3):
         raise ValueError(f"{fn}: x must be a CUDA tensor [rows, heads, d] or [rows, d]")
     dev, shape = x.device, x.shape
-    rows, heads = shape[0], 1 if len(shape) == 2 else shape[1]
     xp = _want(fn, "x", x, torch.bfloat16, dev, (*shape[:-1], plan.d))
-    pp = _want(fn, "pos", pos, torch.int32, dev, (rows,))
-    with _on(dev, stream) as s:
-        out = torch.empty_like(x) if out is None else out
+    pp = _want(fn, "pos", pos, torch.int32, dev, shape[:1])
+    yp = None
+    if out is not None:
         yp = _want(fn, "out", out, torch.bfloat16, dev, shape)
         if yp != xp and abs(yp - xp) < x.numel() * 2:
             raise ValueError(f"{fn}: out overlaps x without being x")
-        _check(fn, _lib.hisa_rope(plan, xp, yp, pp, rows, heads, 1 if transpose else 0, s))
+    return _run(dev, stream, _rope, plan, x, out, xp, yp, pp, shape[0], 1 if len(shape) == 2 else shape[1], transpose)
+
+
+def _rope(s, plan, x, out, xp, yp, pp, rows, heads, transpose):
+    if out is None:
+        out = torch.empty_like(x)
+        yp = out.data_ptr()
+    _check("hisa_rope", _lib.hisa_rope(plan, xp, yp, pp, rows, heads, 1 if transpose else 0, s))
     return out
 
 
@@ -838,8 +852,11 @@ def hisa_cache_store(c: AttnCache, K: torch.Tensor, V: torch.Tensor, seq: torch.
     n, sp, pp = _cache_names(fn, c, seq, pos)
     shape = (n, c.heads, c.d)
     kp, vp = _want(fn, "K", K, torch.bfloat16, dev, shape), _want(fn, "V", V, torch.bfloat16, dev, shape)
-    with _on(dev, stream) as s:
-        _check(fn, _lib.hisa_cache_store(c.struct, kp, vp, sp, pp, n, s))
+    _run(dev, stream, _cache_store, c, kp, vp, sp, pp, n)
+
+
+def _cache_store(s, c, kp, vp, sp, pp, n):
+    _check("hisa_cache_store", _lib.hisa_cache_store(c.struct, kp, vp, sp, pp, n, s))
 
 
 def hisa_cache_load(c: AttnCache, seq: torch.Tensor, pos: Optional[torch.Tensor] = None,
@@ -848,11 +865,19 @@ def hisa_cache_load(c: AttnCache, seq: torch.Tensor, pos: Optional[torch.Tensor]
     fn, dev = "hisa_cache_load", c.device
     n, sp, pp = _cache_names(fn, c, seq, pos)
     shape = (n, c.heads, c.d)
-    with _on(dev, stream) as s:
-        K = torch.empty(shape, dtype=torch.bfloat16, device=dev) if K is None else K
-        V = torch.empty(shape, dtype=torch.bfloat16, device=dev) if V is None else V
-        kp, vp = _want(fn, "K", K, torch.bfloat16, dev, shape), _want(fn, "V", V, torch.bfloat16, dev, shape)
-        _check(fn, _lib.hisa_cache_load(c.struct, kp, vp, sp, pp, n, s))
+    kp = None if K is None else _want(fn, "K", K, torch.bfloat16, dev, shape)
+    vp = None if V is None else _want(fn, "V", V, torch.bfloat16, dev, shape)
+    return _run(dev, stream, _cache_load, c, K, V, kp, vp, sp, pp, n)
+
+
+def _cache_load(s, c, K, V, kp, vp, sp, pp, n):
+    if K is None:
+        K = torch.empty((n, c.heads, c.d), dtype=torch.bfloat16, device=c.device)
+        kp = K.data_ptr()
+    if V is None:
+        V = torch.empty_like(K)
+        vp = V.data_ptr()
+    _check("hisa_cache_load", _lib.hisa_cache_load(c.struct, kp, vp, sp, pp, n, s))
     return K, V
 
 
@@ -880,15 +905,23 @@ def hisa_block_attn(c: AttnCache, Qa: torch.Tensor, q_seq: torch.Tensor, q_pos: 
         if mb < 1:
             raise ValueError(f"{fn}: blocks must have a column (None: the whole prefix)")
     scale = (1.0 / d ** 0.5) if scale is None else float(scale)
-    with _on(dev, stream) as s:
-        if ws is None:
-            ws = workspace(hisa_block_attn_workspace_bytes(c, n_q, Hq, B, mb), dev)
-        wp = _want_ws(fn, ws, dev)
-        out = torch.empty((n_q, Hq, d), dtype=torch.bfloat16, device=dev) if out is None else out
-        lse = torch.empty((n_q, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        op = _want(fn, "out", out, torch.bfloat16, dev, (n_q, Hq, d))
-        lp = _want(fn, "lse", lse, torch.float32, dev, (n_q, Hq))
-        _check(fn, _lib.hisa_block_attn(c.struct, qp, Hq, sp, pp, n_q, bp, mb, B, scale, op, lp, wp, ws.numel(), s))
+    op = None if out is None else _want(fn, "out", out, torch.bfloat16, dev, (n_q, Hq, d))
+    lp = None if lse is None else _want(fn, "lse", lse, torch.float32, dev, (n_q, Hq))
+    return _run(dev, stream, _block_attn, c, Qa, Hq, n_q, B, mb, scale, ws, out, lse, qp, sp, pp, bp, op, lp)
+
+
+def _block_attn(s, c, Qa, Hq, n_q, B, mb, scale, ws, out, lse, qp, sp, pp, bp, op, lp):
+    fn, dev = "hisa_block_attn", c.device
+    if ws is None:
+        ws = workspace(hisa_block_attn_workspace_bytes(c, n_q, Hq, B, mb), dev)
+    wp = _want_ws(fn, ws, dev)
+    if out is None:
+        out = torch.empty_like(Qa)
+        op = out.data_ptr()
+    if lse is None:
+        lse = torch.empty((n_q, Hq), dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    _check(fn, _lib.hisa_block_attn(c.struct, qp, Hq, sp, pp, n_q, bp, mb, B, scale, op, lp, wp, ws.numel(), s))
     return out, lse
 
 
