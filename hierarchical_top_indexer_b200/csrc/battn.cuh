@@ -104,9 +104,27 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // A run's place: key head h, group g, tiles [t0, t0 + n) of the group's T.
+// (p.direct: of the row g at position pos of sequence seq).
 struct BaSeg {
     int h, g, t0, n, T;
+    int seq, pos;
 };
+
+// Tiles of group g.  p.direct: a lone row over its whole prefix has the pieces
+// 0, 1, 2, ... of its sequence, and needs no plan.
+__device__ __forceinline__ int ba_tiles(const BattnParams& p, int g, int* seq, int* pos) {
+    if (!p.direct) return __ldcg(p.tiles + g);
+    *pos = query_position(p.q_seq, p.q_pos, p.len, p.batch, p.cap, g, seq);
+    return *pos >= 0 ? *pos / 128 + 1 : 0;
+}
+
+__device__ __forceinline__ int ba_pieces(const BattnParams& p, const BaSeg& s) { return p.direct ? s.T : p.pieces[s.g]; }
+
+// Piece e of the segment's group: {sequence << 8 | tokens of it that a row sees, piece}.
+__device__ __forceinline__ int2 ba_piece(const BattnParams& p, const BaSeg& s, int e) {
+    if (p.direct) return make_int2(s.seq << 8 | min(128, s.pos + 1 - 128 * e), e);
+    return p.list[static_cast<size_t>(s.g) * p.lcap + e];
+}
 
 // The CTA's run [at, end) of all (key head, group, tile) slots; b0: tiles of
 // the groups before g.
@@ -117,10 +135,10 @@ struct BaCursor {
     __device__ __forceinline__ bool next(const BattnParams& p, BaSeg* s) {
         if (at >= end) return false;
         const int x = static_cast<int>(at - static_cast<long long>(h) * tot);
-        int T = __ldcg(p.tiles + g);
+        int T = ba_tiles(p, g, &s->seq, &s->pos);
         while (x >= b0 + T) {   // done with, or empty
             b0 += T;
-            T = __ldcg(p.tiles + ++g);
+            T = ba_tiles(p, ++g, &s->seq, &s->pos);
         }
         s->h = h;
         s->g = g;
@@ -145,7 +163,12 @@ __device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch)
     const int per = (p.groups + n - 1) / n;
     const int g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
     int sum = 0;
-    for (int g = g0; g < g1; ++g) sum += __ldcg(p.tiles + g);
+    int seq, pos;
+    for (int g = g0; g < g1; ++g) {
+        const int T = ba_tiles(p, g, &seq, &pos);
+        sum += T;
+        if (p.direct && T == 0 && blockIdx.x == 0) set_status(p.status, HISA_DEV_BAD_QUERY);
+    }
     int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,11 +194,11 @@ __device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch)
     if (blockIdx.x == 0) {
         int b = before;
         if (tid == 0) p.tile0[0] = 0;
-        for (int g = g0; g < g1; ++g) p.tile0[g + 1] = b += __ldcg(p.tiles + g);
+        for (int g = g0; g < g1; ++g) p.tile0[g + 1] = b += ba_tiles(p, g, &seq, &pos);
     }
     if (sum > 0 && at >= before && at < before + sum) {
         int g = g0, b = before;
-        while (at >= b + __ldcg(p.tiles + g)) b += __ldcg(p.tiles + g++);
+        for (int T; at >= b + (T = ba_tiles(p, g, &seq, &pos)); ++g) b += T;
         scratch[32] = g;
         scratch[33] = b;
     }

@@ -198,8 +198,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const uint32_t to = tmem + lane_off + L::tmem_o + set * kBdN;
         uint32_t it0 = 0, seg = 0, mn = 0;                // tiles before the segment, segments, uses of mbar
         while (ok && cur.next(p, &sg)) {
-            const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
-            const int np = p.pieces[sg.g];
+            const int np = ba_pieces(p, sg);
             float l[kBdN];
 #pragma unroll
             for (int h = 0; h < kBdN; ++h) l[h] = 0.f;
@@ -207,14 +206,14 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
             __syncwarp();
             const int j0 = (set + kSets - static_cast<int>(it0 % kSets)) % kSets;   // this set's first tile
             int e = (sg.t0 + j0) * p.S + piece;
-            int nv = e < np ? list[e].x & 255 : 0;        // visible tokens of this thread's piece
+            int nv = e < np ? ba_piece(p, sg, e).x & 255 : 0;        // visible tokens of this thread's piece
             for (int j = j0; j < sg.n; j += kSets) {
                 const uint32_t it = it0 + j, buf = it % kBufs, sb = it % kSB;
                 const bool first = j < kSets;
                 const bool vis = in_piece < nv;
                 const bool tail = nv < p.PB;
                 e += kSets * p.S;
-                const int nv_next = e < np ? list[e].x & 255 : 0;
+                const int nv_next = e < np ? ba_piece(p, sg, e).x & 255 : 0;
                 const uint32_t ts = tmem + lane_off + L::tmem_s + sb * kBdN;
                 uint8_t* prow = smem + L::p0 + buf * (kBdN * 256) + tok * 32;
                 if (!(ok = warp_wait_b(sfull + sb, (it / kSB) & 1, abort_flag))) break;
@@ -503,17 +502,16 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const int ch = lane % kCh, rl = lane / kCh;
         uint32_t it0 = 0;   // tiles before the segment
         while (ok && cur.next(p, &sg)) {
-            const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
-            const int np = p.pieces[sg.g];
+            const int np = ba_pieces(p, sg);
             const int r = dw * 32 + lane, s = r / p.PB;
             const int j0 = (team + 2 - static_cast<int>(it0 & 1)) & 1;
             int e = (sg.t0 + j0) * p.S + s;
-            bool sees = e < np && r - s * p.PB < (list[min(e, np - 1)].x & 255);
+            bool sees = e < np && r - s * p.PB < (ba_piece(p, sg, min(e, np - 1)).x & 255);
             for (int j = j0; j < sg.n; j += 2) {
                 const uint32_t it = it0 + j;
                 const uint32_t seen = __ballot_sync(0xffffffffu, sees);   // the other rows become zeros
                 e += 2 * p.S;
-                sees = e < np && r - s * p.PB < (list[min(e, np - 1)].x & 255);
+                sees = e < np && r - s * p.PB < (ba_piece(p, sg, min(e, np - 1)).x & 255);
                 const uint32_t rs = it % kRaw, slot = it % kS;
                 if (!(ok = warp_wait_b(rfull + rs, (it / kRaw) & 1, abort_flag))) break;
                 // the slot's last reader, P V of tile it - kS (this team saw the one before it - kS + 1
@@ -565,8 +563,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         // Lane s < S loads piece s of each tile.
         uint32_t it = 0, seg = 0, issued = 0;
         while (ok && cur.next(p, &sg)) {
-            const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
-            const int np = p.pieces[sg.g];
+            const int np = ba_pieces(p, sg);
             if (!FP4) {
                 if (seg > 0 && !(ok = warp_wait_b(qempty, (seg - 1) & 1, abort_flag))) break;
                 if (lane == 0) {
@@ -580,11 +577,11 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
             ++seg;
             int e = sg.t0 * p.S + lane;
             const bool mine = lane < p.S;
-            int2 pc = mine && e < np ? list[e] : make_int2(-1, 0);
+            int2 pc = mine && e < np ? ba_piece(p, sg, e) : make_int2(-1, 0);
             for (int j = 0; j < sg.n; ++j, ++it) {
                 const int2 now = pc;
                 e += p.S;
-                pc = mine && j + 1 < sg.n && e < np ? list[e] : make_int2(-1, 0);
+                pc = mine && j + 1 < sg.n && e < np ? ba_piece(p, sg, e) : make_int2(-1, 0);
                 const bool have = now.x >= 0;
                 const int bh = have ? (now.x >> 8) * p.Hkv + sg.h : 0;
                 if (!FP4) {

@@ -253,6 +253,7 @@ cudaError_t launch_cache_load(const CacheParams& p, cudaStream_t s);
 // Block-sparse attention (battn.cu).
 constexpr int kBattnMaxSms = 148;    // SMs whose CTAs' partial outputs the workspace holds
 constexpr int kBattnDecHeads = 16;   // most heads per key head of the single-row kernel
+constexpr int kBattnDirectRows = 1024;
 struct BattnParams {
     const uint16_t* q;       // [n_q, Hq, d] bf16
     const int32_t* q_seq;    // [n_q]
@@ -279,6 +280,7 @@ struct BattnParams {
     int* tile0;              // [groups + 1] tiles of the groups before (for join_kernel)
     uint32_t* bits;          // [n_q, W] (R > 1)
     int dec, prow;           // the single-row kernel serves the call; rows of a part
+    int direct;              // and works out the pieces itself (no plan)
     float* part_o;           // [2 * grid, prow, d]
     float2* part_ml;         // [2 * grid, prow] maximum (log2 domain) and sum
 };
