@@ -16,14 +16,16 @@
 // rows and all or some of their heads; it issues its loads first (up to four
 // tasks of one or two 16-byte chunks per thread), computes the sine and cosine
 // of each (row, pair) once while they are in flight, and every head of the
-// row uses them.
+// row uses them.  4096 rows of 64 heads of 128, 64 of them rotated: 24.7 us,
+// 84% of the measured copy rate; with 256 threads a block 27.0 us, with 64
+// threads of eight tasks 31.6 us (small blocks load while others store).
 #include "hisa_kernels.cuh"
 
 namespace hisa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeTasks = 4;          // per thread
 constexpr int kRopeMaxSc = 1024;       // (row, pair) sine and cosine entries per block
 
