@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    BaCursor cur = ba_start(p, reinterpret_cast<int*>(smem + L::ml));
+    BaCursor cur = ba_start<false>(p, reinterpret_cast<int*>(smem + L::ml));
     BaSeg sg;
     bool ok = true;
 
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         // ------------------------------------------------------------ load
         // Lane s < S loads piece s of each tile.
         uint32_t it = 0, seg = 0, issued[2] = {0, 0};
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<false>(p, &sg)) {
             const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
             const int np = p.pieces[sg.g];
             if (!FP4) {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
             ++kn;
             return true;
         };
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<false>(p, &sg)) {
             if (!(ok = warp_wait_b(qfull, seg & 1, abort_flag))) break;
             tc_fence_after();
             ok = issue_s(0) && (sg.n < 2 || issue_s(1));
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         float2* ml = reinterpret_cast<float2*>(smem + L::ml);
         const float* qs = reinterpret_cast<const float*>(smem + L::qs);
         uint32_t sn = 0, seg = 0, vbase = 0;
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<false>(p, &sg)) {
             const int row = sg.g * p.R + rr;
             const bool live = rr < p.R && row < p.n_q;
             int b = -1, t = -1;
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(BaLayout<D, FP4>::threads, 1)
         // ------------------------------------------------------ dequantise
         const int dw = warp - kBaWarpDeq;
         uint32_t it = 0, seg = 0;
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<false>(p, &sg)) {
             const int2* list = p.list + static_cast<size_t>(sg.g) * p.lcap;
             const int np = p.pieces[sg.g];
             if (seg > 0 && !(ok = warp_wait_b(qempty, (seg - 1) & 1, abort_flag))) break;

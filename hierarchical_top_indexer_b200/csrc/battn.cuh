@@ -111,9 +111,11 @@ struct BaSeg {
 };
 
 // Tiles of group g.  p.direct: a lone row over its whole prefix has the pieces
-// 0, 1, 2, ... of its sequence, and needs no plan.
+// 0, 1, 2, ... of its sequence, and needs no plan.  LONE: the kernel may be
+// asked for that.
+template <bool LONE>
 __device__ __forceinline__ int ba_tiles(const BattnParams& p, int g, int* seq, int* pos) {
-    if (!p.direct) return __ldcg(p.tiles + g);
+    if (!LONE || !p.direct) return __ldcg(p.tiles + g);
     *pos = query_position(p.q_seq, p.q_pos, p.len, p.batch, p.cap, g, seq);
     return *pos >= 0 ? *pos / 128 + 1 : 0;
 }
@@ -132,13 +134,14 @@ struct BaCursor {
     long long at, end;
     int tot, h, g, b0;
 
+    template <bool LONE>
     __device__ __forceinline__ bool next(const BattnParams& p, BaSeg* s) {
         if (at >= end) return false;
         const int x = static_cast<int>(at - static_cast<long long>(h) * tot);
-        int T = ba_tiles(p, g, &s->seq, &s->pos);
+        int T = ba_tiles<LONE>(p, g, &s->seq, &s->pos);
         while (x >= b0 + T) {   // done with, or empty
             b0 += T;
-            T = ba_tiles(p, ++g, &s->seq, &s->pos);
+            T = ba_tiles<LONE>(p, ++g, &s->seq, &s->pos);
         }
         s->h = h;
         s->g = g;
@@ -158,6 +161,7 @@ struct BaCursor {
 // Every thread of the CTA: adds the groups' tiles up and finds the run's
 // start.  scratch: 40 ints of shared memory.  CTA 0 leaves the sums in tile0
 // for join_kernel.
+template <bool LONE>
 __device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch) {
     const int tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31;
     const int per = (p.groups + n - 1) / n;
@@ -165,9 +169,9 @@ __device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch)
     int sum = 0;
     int seq, pos;
     for (int g = g0; g < g1; ++g) {
-        const int T = ba_tiles(p, g, &seq, &pos);
+        const int T = ba_tiles<LONE>(p, g, &seq, &pos);
         sum += T;
-        if (p.direct && T == 0 && blockIdx.x == 0) set_status(p.status, HISA_DEV_BAD_QUERY);
+        if (LONE && p.direct && T == 0 && blockIdx.x == 0) set_status(p.status, HISA_DEV_BAD_QUERY);
     }
     int x = sum;
 #pragma unroll
@@ -194,11 +198,11 @@ __device__ __forceinline__ BaCursor ba_start(const BattnParams& p, int* scratch)
     if (blockIdx.x == 0) {
         int b = before;
         if (tid == 0) p.tile0[0] = 0;
-        for (int g = g0; g < g1; ++g) p.tile0[g + 1] = b += ba_tiles(p, g, &seq, &pos);
+        for (int g = g0; g < g1; ++g) p.tile0[g + 1] = b += ba_tiles<LONE>(p, g, &seq, &pos);
     }
     if (sum > 0 && at >= before && at < before + sum) {
         int g = g0, b = before;
-        for (int T; at >= b + (T = ba_tiles(p, g, &seq, &pos)); ++g) b += T;
+        for (int T; at >= b + (T = ba_tiles<LONE>(p, g, &seq, &pos)); ++g) b += T;
         scratch[32] = g;
         scratch[33] = b;
     }

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();
     grid_launch_dependents();
-    BaCursor cur = ba_start(p, reinterpret_cast<int*>(smem + L::refs));
+    BaCursor cur = ba_start<true>(p, reinterpret_cast<int*>(smem + L::refs));
     BaSeg sg;
     bool ok = true;
 
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const int half = ((tok >> 2) & 1) << 4;
         const uint32_t to = tmem + lane_off + L::tmem_o + set * kBdN;
         uint32_t it0 = 0, seg = 0, mn = 0;                // tiles before the segment, segments, uses of mbar
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             const int np = ba_pieces(p, sg);
             float l[kBdN];
 #pragma unroll
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const int dw = warp - L::warp_kd;
         const int row = dw * 32 + lane;
         uint32_t it = 0, seg = 0;
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             if (seg > 0 && !(ok = warp_wait_b(qempty, (seg - 1) & 1, abort_flag))) break;
             // the softmax is done with the scales of two segments ago
             if (seg > 1 && !(ok = warp_wait_b(odone + (seg & 1), ((seg >> 1) - 1) & 1, abort_flag))) break;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         constexpr int kRows = 32 / kCh;   // rows a warp expands at a time
         const int ch = lane % kCh, rl = lane / kCh;
         uint32_t it0 = 0;   // tiles before the segment
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             const int np = ba_pieces(p, sg);
             const int r = dw * 32 + lane, s = r / p.PB;
             const int j0 = (team + 2 - static_cast<int>(it0 & 1)) & 1;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         // ------------------------------------------------------------ load
         // Lane s < S loads piece s of each tile.
         uint32_t it = 0, seg = 0, issued = 0;
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             const int np = ba_pieces(p, sg);
             if (!FP4) {
                 if (seg > 0 && !(ok = warp_wait_b(qempty, (seg - 1) & 1, abort_flag))) break;
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const uint32_t q_lo = uni(desc_lo(smem_addr(smem + L::q), 16)), k_lo = uni(desc_lo(smem_addr(smem + L::ring), 16));
         const uint32_t tm = uni(tmem);
         uint32_t it = 0, seg = 0;
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             if (!(ok = warp_wait_b(qfull, seg & 1, abort_flag))) break;
             for (int j = 0; j < sg.n; ++j, ++it) {
                 const uint32_t sb = it % kSB, slot = (2 * it) % kS;
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(BdLayout<D, FP4>::warps * 32, BdLayout<D, FP4>
         const uint32_t v_lo = uni(desc_lo(smem_addr(smem + L::ring), D == 128 ? 16384 : 1024));
         const uint32_t p_lo = uni(desc_lo(smem_addr(smem + L::p0), 16)), tm = uni(tmem);
         uint32_t it = 0, seg = 0, fixes[2] = {0, 0};
-        while (ok && cur.next(p, &sg)) {
+        while (ok && cur.next<true>(p, &sg)) {
             for (int j = 0; j < sg.n; ++j, ++it) {
                 const uint32_t buf = it % kBufs, set = it % kSets, n = FP4 ? it : 2 * it + 1, slot = n % kS;
                 if (!(ok = warp_wait_b(pfull + buf, (it / kBufs) & 1, abort_flag))) break;
