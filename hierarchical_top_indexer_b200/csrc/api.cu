@@ -770,6 +770,12 @@ bool gathered_level(int bf, int W, int nblk, int n_q) {
 
 // ---------------------------------------------------- the attention's cache
 
+// Two ranges of the same size that share a byte.
+bool overlap(const void* a, const void* b, unsigned long long bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x < y ? y - x : x - y) < bytes;
+}
+
 bool power_of_two(float x) {
     int e;
     return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e >= -59 && e <= 61;
@@ -1395,6 +1401,7 @@ int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, do
     plan->off = off;
     plan->layout = layout;
     plan->gain = static_cast<float>(gain != 0.0 ? gain : scaling == HISA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0);
+    if (!std::isfinite(plan->gain)) return HISA_E_INVAL;
     plan->ready = 1;
     return HISA_OK;
 }
@@ -1407,6 +1414,7 @@ int hisa_rope(const hisa_rope_plan* plan, const uint16_t* x, uint16_t* y, const 
         return HISA_E_INVAL;
     if (rows == 0) return HISA_OK;
     if (!x || !y || !pos || !aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return HISA_E_INVAL;
+    if (x != y && overlap(x, y, 2ull * rows * heads * plan->d)) return HISA_E_INVAL;
     const int sms = sm_count();
     if (sms <= 0) return HISA_E_CUDA;
     RopeParams p;
@@ -1474,6 +1482,8 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
         (q_pos && !aligned(q_pos, 4)) || (blocks && !aligned(blocks, 4)) || (lse && !aligned(lse, 4)))
         return HISA_E_INVAL;
     if (!ws || !aligned(ws, 256) || ws_bytes < need) return HISA_E_WORKSPACE;
+    // a row's output may be written while another CTA has yet to read its queries
+    if (overlap(Qa, out, 2ull * n_q * Hq * c->d)) return HISA_E_INVAL;
     const bool fp4 = c->dtype == HISA_CACHE_FP4;
     p.q = Qa;
     p.q_seq = q_seq;

@@ -32,7 +32,7 @@
 //
 // Bound (d = 128): bf16 rows by HBM, 64 rows of 8192 kept keys and 8 key heads
 // in 338 us, 6.4 TB/s.  4-bit rows: 16 prefixes of about 115K keys and 4 key
-// heads in 277 to 292 us, 3.7 TB/s; 211 us of it remain when neither the
+// heads in 278 to 300 us, 3.7 TB/s; 211 us of it remain when neither the
 // expanding nor the softmax does anything, so the hand-over from stage to
 // stage bounds it (shared memory moves about 110 KB a tile, 860 of the 1360
 // cycles a tile takes).

@@ -428,7 +428,7 @@ int hisa_select_blocks(const hisa_kv* kv, const uint16_t* Q, const float* w, con
  *                    lo = max(floor(c(beta_fast)), 0) and
  *                    hi = min(ceil(c(beta_slow)), rot - 1), where
  *                    c(t) = rot ln(orig_len / (2 pi t)) / (2 ln base)
- *   gain     g; 0: the scaling's own, 0.1 ln(factor) + 1 for YARN, else 1
+ *   gain     g, in fp32's range; 0: the scaling's own, 0.1 ln(factor) + 1 for YARN, else 1
  * factor >= 1; base > 1; YARN: orig_len > 0, beta_fast >= beta_slow > 0.
  * Angles are exact to about 2^-31 of a turn at every 32-bit position,
  * negative ones included.
@@ -509,7 +509,8 @@ typedef struct hisa_attn_kv {
  * quantised: per 16 elements scale = e4m3(min(448, max|x| / (6 mul))), code =
  * e2m1(x / (mul * scale)), both to nearest with ties to even, codes saturated
  * at 6.  Each (seq, pos) may be named once in a call; which row a position
- * named twice holds afterwards is undefined (it may mix them).  A token with a
+ * named twice holds afterwards is undefined (it may mix them).  K and V lie
+ * outside the cache's own rows (in hisa_cache_load too).  A token with a
  * bad sequence (HISA_DEV_BAD_QUERY) or position (HISA_DEV_CAPACITY) is skipped.
  * hisa_cache_load — the way back: K, V [n, heads, d] bf16 out, the values the
  * cache's rows stand for; a zero row and a status bit for a bad name.
@@ -537,7 +538,8 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  *          output of hisa_select_blocks or hisa_select_inspect); entries that
  *          are negative or lie past the row's position are skipped, a repeated
  *          id counts once.  NULL with mb = 0: the whole prefix (B is not read)
- *   out    [n_q, Hq, d] bf16; lse [n_q, Hq] fp32 or NULL
+ *   out    [n_q, Hq, d] bf16, which may not overlap Qa; lse [n_q, Hq] fp32 or
+ *          NULL
  *   ws     workspace of at least hisa_block_attn_workspace_bytes(...) bytes
  * A row that sees no token gives out = 0 and lse = -inf; a row whose position
  * is not inside its prefix does too, and sets HISA_DEV_BAD_QUERY.  Sizes: B as

@@ -167,3 +167,20 @@ def test_the_binding_refuses_tensors_the_call_cannot_read():
             hisa.hisa_cache_store(c, **{**dict(K=rows, V=rows, seq=seq), **bad})
     with pytest.raises(ValueError):
         hisa.hisa_rope(hisa.hisa_rope_init(64), rows, seq)      # not a CUDA tensor
+
+
+def test_outputs_that_overlap_their_inputs_are_refused():
+    c = _kv()
+    size = 4 * 16 * 128 * 2   # n_q rows of Hq heads
+    for out in (1 << 20, (1 << 20) + size - 16, (1 << 20) - size + 16):
+        assert _attn(c, Qa=P(1 << 20), out=P(out)) == hisa.HISA_E_INVAL, out
+    lib, p = hisa.lib(), hisa.hisa_rope_init(64)
+    size = 4 * 2 * 64 * 2
+    for y in ((1 << 20) + 16, (1 << 20) + size - 16, (1 << 20) - size + 16):
+        assert lib.hisa_rope(ctypes.byref(p), P(1 << 20), P(y), P(16), 4, 2, 0, None) == hisa.HISA_E_INVAL, y
+
+
+def test_a_gain_past_fp32_is_refused():
+    with pytest.raises(hisa.HisaError) as e:
+        hisa.hisa_rope_init(64, gain=1e39)
+    assert e.value.code == hisa.HISA_E_INVAL
