@@ -252,8 +252,28 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const uin
         }
         tmem_st16(ts + c * 16, w);
     }
-    l += (s0 + s1) + (s2 + s3);
+    float sum = (s0 + s1) + (s2 + s3);
     tmem_st_wait();
+    if (!MASK && !FP4) {
+        // An off row's weights are 2^(0 S - 200) = 0, and so is their sum, unless S overflowed
+        // fp32 (bf16 rows: products of 4-bit rows stay far below): 0 * inf is NaN.  Then the off
+        // rows' P is cleared after all (S is gone, so the warp cannot go through the masked form
+        // again; a vote a tile, no work per element).
+        if (__any_sync(0xffffffffu, off && sum != 0.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+                tmem_ld16_nowait(ts + c * 16, w);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = off ? 0u : w[i];
+                tmem_st16(ts + c * 16, w);
+            }
+            tmem_st_wait();
+            if (off) sum = 0.f;
+        }
+    }
+    l += sum;
 }
 
 template <int D, bool FP4>

@@ -546,9 +546,11 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  * hisa_select, at most 2^20 blocks per sequence, G in 1..128, scale positive
  * and, times k_mul, in fp32's range.
  * Numerics: logits from exact products (bf16, or f16 for FP4 rows) summed in
- * fp32; softmax maxima and sums in fp32; the weights are rounded to bf16 (f16
- * for FP4 rows) for the product with the values, accumulated in fp32; out is
- * rounded once to bf16.  Results do not depend on the order of atomics.
+ * fp32, whose range those of the tokens a row sees must stay in (another
+ * row's may leave it); softmax maxima and sums in fp32; the weights are
+ * rounded to bf16 (f16 for FP4 rows) for the product with the values,
+ * accumulated in fp32; out is rounded once to bf16.  Results do not depend on
+ * the order of atomics.
  * Errors: HISA_E_INVAL, HISA_E_UNSUPPORTED, HISA_E_WORKSPACE, HISA_E_CUDA.
  */
 size_t hisa_block_attn_workspace_bytes(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb);
