@@ -1476,8 +1476,9 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
     size_t need = 0;
     rc = battn_params(c, n_q, Hq, B, mb, ws, &p, &need);
     if (rc) return rc;
-    if (!(scale > 0.f) || !std::isfinite(scale) || (mb > 0) != (blocks != nullptr)) return HISA_E_INVAL;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return HISA_E_INVAL;
     if (n_q == 0) return HISA_OK;
+    if ((mb > 0) != (blocks != nullptr)) return HISA_E_INVAL;
     if (!Qa || !q_seq || !out || !aligned(Qa, 16) || !aligned(out, 16) || !aligned(q_seq, 4) ||
         (q_pos && !aligned(q_pos, 4)) || (blocks && !aligned(blocks, 4)) || (lse && !aligned(lse, 4)))
         return HISA_E_INVAL;

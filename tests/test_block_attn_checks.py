@@ -184,3 +184,12 @@ def test_a_gain_past_fp32_is_refused():
     with pytest.raises(hisa.HisaError) as e:
         hisa.hisa_rope_init(64, gain=1e39)
     assert e.value.code == hisa.HISA_E_INVAL
+
+
+def test_an_empty_batch_with_kept_blocks_is_no_error():
+    """A tensor without elements has no address: hisa_select_blocks of no rows gives such a list."""
+    assert torch.zeros((0, 8), dtype=torch.int32).data_ptr() == 0
+    for c in (_kv(), _fp4()):
+        assert _attn(c, n_q=0, blocks=None, mb=8, Qa=None, q_seq=None, out=None, ws=None, ws_bytes=0) == hisa.HISA_OK
+        assert _attn(c, n_q=0, blocks=None, mb=8, B=12) == hisa.HISA_E_UNSUPPORTED     # sizes are checked all the same
+        assert _attn(c, n_q=1, blocks=None, mb=8) == hisa.HISA_E_INVAL

@@ -39,3 +39,20 @@ def test_unseen_logits_past_fp32(d, G, B, every):
     r = ref.block_attn(_f64(q), _f64(k), _f64(v), np.zeros(n, int), pos, blocks, B, 1 / math.sqrt(d))
     assert r["zabs"].max() < 64
     ref.check_block_attn(_f64(out), _f64(lse), r, d, False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp4"])
+def test_select_then_attend_with_no_rows(dtype):
+    kv = hisa.KVCache(2, 256, 128, 64)
+    kv.len.fill_(256)
+    hisa.hisa_pool_blocks(kv)
+    c = hisa.AttnCache(2, 256, 1, 128, dtype, lens=kv.len, status=kv.status)
+    none = _i32([])
+    blocks = hisa.hisa_select_blocks(kv, torch.zeros((0, 16, 128), dtype=torch.bfloat16, device="cuda"),
+                                     torch.zeros((0, 16), device="cuda"), none, none, 3)
+    assert blocks.shape == (0, 3)
+    Qa = torch.zeros((5, 4, 128), dtype=torch.bfloat16, device="cuda")
+    for pos in (none, None):
+        out, lse = hisa.hisa_block_attn(c, Qa[:0], none, pos, blocks, B=64)
+        assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    assert kv.status_bits() == 0
