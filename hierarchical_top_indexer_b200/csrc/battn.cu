@@ -843,10 +843,10 @@ cudaError_t launch_typed(const CUtensorMap& qm, const CUtensorMap& km, const CUt
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const size_t bits = p.blocks && p.R == 1 ? static_cast<size_t>(p.W) * 4 : 0;
-    e = smem_limit(reinterpret_cast<const void*>(plan_kernel), bits);
-    if (e != cudaSuccess) return e;
     if (!p.direct) {
+        const size_t bits = p.blocks && p.R == 1 ? static_cast<size_t>(p.W) * 4 : 0;
+        e = smem_limit(reinterpret_cast<const void*>(plan_kernel), bits);
+        if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(static_cast<unsigned>(p.groups));
         cfg.blockDim = dim3(kPlanThreads);
         cfg.dynamicSmemBytes = bits;

@@ -296,7 +296,9 @@ cudaError_t launch_wait_probe(uint32_t* status, cudaStream_t s);
 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device, once: the attribute call costs microseconds of host time,
-// so it is made only the first time a kernel needs a larger limit there.
+// so it is made only the first time a kernel needs a larger limit there.  The
+// lock is held until the attribute is set: host threads that ask for
+// different sizes at once could otherwise lower it behind the record.
 // (A cudaDeviceReset discards the attribute but not this record; a process
 // that resets a device it keeps using would see the next large launch fail
 // with an invalid-value error.)
@@ -306,17 +308,12 @@ inline cudaError_t smem_limit(const void* fn, size_t bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> g(mu);
-        const auto it = have.find({fn, dev});
-        if (it != have.end() && it->second >= bytes) return cudaSuccess;
-    }
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> g(mu);
-    size_t& h = have[{fn, dev}];
-    if (h < bytes) h = bytes;
-    return cudaSuccess;
+    size_t& h = have[{fn, dev}];   // 0 at first, which every kernel's limit covers
+    if (h >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) h = bytes;
+    return e;
 }
 
 cudaError_t launch_pool(const KvView& kv, cudaStream_t s);
