@@ -53,8 +53,8 @@ EXPORTS = ("hisa_pool_blocks", "hisa_append", "hisa_select_workspace_bytes", "hi
            "hisa_cp_workspace_bytes", "hisa_cp_blocks",
            "hisa_cp_tokens", "hisa_merge_topk", "hisa_sparse_attn_workspace_bytes", "hisa_sparse_attn",
            "dsa_flat_workspace_bytes", "dsa_flat_select", "hisa_topk_f32",
-           "hisa_profile_enable", "hisa_profile_read", "hisa_status_string", "hisa_last_cuda_error",
-           "hisa_selftest_wait",
+           "hisa_profile_enable", "hisa_profile_read", "hisa_profile_read_n", "hisa_status_string",
+           "hisa_last_cuda_error", "hisa_selftest_wait",
            "hisa_select_blocks_workspace_bytes", "hisa_select_blocks", "hisa_rope_init", "hisa_rope",
            "hisa_cache_store", "hisa_cache_load", "hisa_block_attn_workspace_bytes", "hisa_block_attn")
 PHASES = ("block_score", "block_select", "token_score", "token_select", "flat_score",
@@ -136,6 +136,7 @@ _lib.hisa_selftest_wait.argtypes = [_P, _P]
 _lib.hisa_selftest_wait.restype = _I
 _lib.hisa_profile_enable.argtypes = [_I]
 _lib.hisa_profile_read.argtypes = [_P, _P, _I]
+_lib.hisa_profile_read_n.argtypes = [_P, _P, _I, _I]
 _lib.hisa_status_string.argtypes = [_I]
 _lib.hisa_status_string.restype = ctypes.c_char_p
 _lib.hisa_last_cuda_error.argtypes = []
@@ -145,7 +146,7 @@ for _f in ("hisa_pool_blocks", "hisa_append", "hisa_select", "hisa_decode_step",
            "hisa_tree_select", "hisa_pool_tail", "hisa_levels_select", "hisa_cp_blocks", "hisa_cp_tokens",
            "hisa_merge_topk",
            "hisa_sparse_attn", "dsa_flat_select", "hisa_topk_f32", "hisa_profile_enable", "hisa_profile_read",
-           "hisa_select_blocks", "hisa_rope_init", "hisa_rope", "hisa_cache_store", "hisa_cache_load",
+           "hisa_profile_read_n", "hisa_select_blocks", "hisa_rope_init", "hisa_rope", "hisa_cache_store", "hisa_cache_load",
            "hisa_block_attn"):
     getattr(_lib, _f).restype = _I
 
@@ -967,5 +968,5 @@ def hisa_profile_read(reset: bool = True) -> dict:
     """{phase: (milliseconds, launches)} accumulated since the last reset."""
     ms = (ctypes.c_float * len(PHASES))()
     n = (ctypes.c_int * len(PHASES))()
-    _check("hisa_profile_read", _lib.hisa_profile_read(ms, n, 1 if reset else 0))
+    _check("hisa_profile_read_n", _lib.hisa_profile_read_n(ms, n, len(PHASES), 1 if reset else 0))
     return {name: (float(ms[i]), int(n[i])) for i, name in enumerate(PHASES)}

@@ -1608,17 +1608,23 @@ int hisa_profile_enable(int on) {
 }
 
 int hisa_profile_read(float* ms, int* launches, int reset) {
+    return hisa_profile_read_n(ms, launches, HISA_NUM_PHASES, reset);
+}
+
+int hisa_profile_read_n(float* ms, int* launches, int n, int reset) {
+    if (n < 0) return HISA_E_INVAL;
     Profiler& P = profiler();
     std::lock_guard<std::mutex> g(P.mu);
-    if (ms)
-        for (int i = 0; i < HISA_NUM_PHASES; ++i) ms[i] = 0.f;
-    if (launches)
-        for (int i = 0; i < HISA_NUM_PHASES; ++i) launches[i] = 0;
+    for (int i = 0; i < n; ++i) {
+        if (ms) ms[i] = 0.f;
+        if (launches) launches[i] = 0;
+    }
     int rc = HISA_OK;
     for (const PhaseEvents& e : P.pending) {
         float t = 0.f;
         if (cudaEventSynchronize(e.stop) != cudaSuccess || cudaEventElapsedTime(&t, e.start, e.stop) != cudaSuccess)
             rc = HISA_E_CUDA;
+        if (e.phase >= n) continue;
         if (ms) ms[e.phase] += t;
         if (launches) launches[e.phase] += 1;
     }

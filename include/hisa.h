@@ -635,7 +635,12 @@ int hisa_topk_f32(const float* x, int rows, int n, int k, int32_t* idx, hisa_str
  * enabled, every call records a CUDA event pair around each kernel it
  * launches, on the call's stream.  hisa_profile_read waits for the recorded
  * events, adds up their durations per phase (milliseconds) and launch counts,
- * and with reset != 0 starts a new accumulation.  Phases:
+ * and with reset != 0 starts a new accumulation (of all phases).  It writes
+ * HISA_NUM_PHASES entries to each array, a number that stays what it is, so
+ * that a program built with an earlier header is not written past its arrays.
+ * hisa_profile_read_n writes n entries (0 for phases that the library does
+ * not have): HISA_NUM_ALL_PHASES of this header for all of them.
+ * HISA_E_INVAL for n < 0.  Phases:
  */
 enum hisa_phase {
     HISA_PHASE_BLOCK_SCORE = 0,   /* stage 1: score block representatives */
@@ -653,10 +658,12 @@ enum hisa_phase {
     HISA_PHASE_ROPE = 12,         /* hisa_rope */
     HISA_PHASE_CACHE = 13,        /* hisa_cache_store, hisa_cache_load */
     HISA_PHASE_BLOCK_ATTN = 14,   /* hisa_block_attn */
-    HISA_NUM_PHASES = 15
+    HISA_NUM_PHASES = 12,         /* of hisa_profile_read: those before HISA_PHASE_ROPE */
+    HISA_NUM_ALL_PHASES = 15
 };
 int hisa_profile_enable(int on);
 int hisa_profile_read(float* ms, int* launches, int reset);
+int hisa_profile_read_n(float* ms, int* launches, int n, int reset);
 
 /*
  * hisa_selftest_wait — failure detection check (no counterpart on the pages).
