@@ -839,6 +839,9 @@ int battn_params(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb, void* ws
     if (n_q < 0 || Hq < 1 || mb < 0) return HISA_E_INVAL;
     if (Hq % c->heads != 0) return HISA_E_INVAL;
     if (Hq / c->heads > 128) return HISA_E_UNSUPPORTED;
+    // the plan's threads count a group's list entries (up to 128 rows') in 32 bits and step up to
+    // 256 past the last
+    if (mb > (1 << 24) - 4) return HISA_E_UNSUPPORTED;
     if (mb > 0 && (!select_block_size_ok(B) || (static_cast<long long>(c->cap) + B - 1) / B > 1 << 20)) return HISA_E_UNSUPPORTED;
     std::memset(p, 0, sizeof *p);
     p->len = c->len;
@@ -854,9 +857,7 @@ int battn_params(const hisa_attn_kv* c, int n_q, int Hq, int B, int mb, void* ws
     *bytes = battn_layout(*p, ws);
     // tile numbers and grids are 32-bit
     const long long tiles = (static_cast<long long>(p->lcap) / p->S + 1) * p->groups;
-    if (p->lcap < 0 || tiles > INT_MAX || static_cast<long long>(p->groups) * p->Hkv > INT_MAX ||
-        static_cast<long long>(p->R) * mb > INT_MAX)
-        return HISA_E_UNSUPPORTED;
+    if (p->lcap < 0 || tiles > INT_MAX || static_cast<long long>(p->groups) * p->Hkv > INT_MAX) return HISA_E_UNSUPPORTED;
     return HISA_OK;
 }
 

@@ -543,8 +543,8 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  *   ws     workspace of at least hisa_block_attn_workspace_bytes(...) bytes
  * A row that sees no token gives out = 0 and lse = -inf; a row whose position
  * is not inside its prefix does too, and sets HISA_DEV_BAD_QUERY.  Sizes: B as
- * hisa_select, at most 2^20 blocks per sequence, G in 1..128, scale positive
- * and, times k_mul, in fp32's range.
+ * hisa_select, at most 2^20 blocks per sequence, mb at most 2^24 - 4, G in
+ * 1..128, scale positive and, times k_mul, in fp32's range.
  * Numerics: logits from exact products (bf16, or f16 for FP4 rows) summed in
  * fp32, whose range those of the tokens a row sees must stay in (another
  * row's may leave it); softmax maxima and sums in fp32; the weights are

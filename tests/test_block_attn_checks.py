@@ -193,3 +193,15 @@ def test_an_empty_batch_with_kept_blocks_is_no_error():
         assert _attn(c, n_q=0, blocks=None, mb=8, Qa=None, q_seq=None, out=None, ws=None, ws_bytes=0) == hisa.HISA_OK
         assert _attn(c, n_q=0, blocks=None, mb=8, B=12) == hisa.HISA_E_UNSUPPORTED     # sizes are checked all the same
         assert _attn(c, n_q=1, blocks=None, mb=8) == hisa.HISA_E_INVAL
+
+
+def test_lists_longer_than_the_plan_counts_are_refused():
+    """The plan counts the entries of up to 128 rows in an int and steps 256 at a time: 128 * mb + 256 < 2^31."""
+    most = (1 << 24) - 4
+    assert 128 * most + 256 < 1 << 31 <= 128 * (most + 4) + 256
+    for make in (_kv, _fp4):
+        for Hq in (2, 16, 256):
+            size = lambda mb: hisa.lib().hisa_block_attn_workspace_bytes(ctypes.byref(make()), 1, Hq, 128, mb)  # noqa: E731,B023
+            assert size(most) > 0
+            for mb in (most + 1, (1 << 31) - 200, (1 << 31) - 1):
+                assert size(mb) == 0 and _attn(make(), Hq=Hq, n_q=1, mb=mb) == hisa.HISA_E_UNSUPPORTED, mb
