@@ -195,8 +195,8 @@ cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s) {
     }
     p.tasks_inv = (1u << 20) / p.tasks + 1;    // x * inv >> 20 = x / tasks for x, tasks below 2^10
     p.heads_inv = (1u << 20) / p.heads_blk + 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((p.rows + p.rows_blk - 1) / p.rows_blk),
-                       static_cast<unsigned>((p.heads + p.heads_blk - 1) / p.heads_blk));
+    cfg.gridDim = dim3(static_cast<unsigned>((p.rows - 1) / p.rows_blk + 1),   // (rows reach INT_MAX)
+                       static_cast<unsigned>((p.heads - 1) / p.heads_blk + 1));
     return half_vec ? cudaLaunchKernelEx(&cfg, rope_vec_kernel<0>, p) : cudaLaunchKernelEx(&cfg, rope_vec_kernel<1>, p);
 }
 
