@@ -770,10 +770,19 @@ bool gathered_level(int bf, int W, int nblk, int n_q) {
 
 // ---------------------------------------------------- the attention's cache
 
-// Two ranges of the same size that share a byte.
-bool overlap(const void* a, const void* b, unsigned long long bytes) {
+// Two ranges that share a byte.
+bool overlap(const void* a, unsigned long long a_bytes, const void* b, unsigned long long b_bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return (x < y ? y - x : x - y) < bytes;
+    return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
+// A range that shares a byte with the cache's rows or scales.
+bool in_cache(const hisa_attn_kv* c, const void* a, unsigned long long bytes) {
+    const bool fp4 = c->dtype == HISA_CACHE_FP4;
+    const unsigned long long elems = static_cast<unsigned long long>(c->batch) * c->heads * c->cap * c->d;
+    const unsigned long long row_bytes = fp4 ? elems / 2 : elems * 2;
+    return overlap(a, bytes, c->k, row_bytes) || overlap(a, bytes, c->v, row_bytes) ||
+           (fp4 && (overlap(a, bytes, c->k_scale, elems / 16) || overlap(a, bytes, c->v_scale, elems / 16)));
 }
 
 bool power_of_two(float x) {
@@ -809,6 +818,8 @@ int check_cache_rows(const hisa_attn_kv* c, const void* K, const void* V, const 
     if (!K || !V || !seq || !aligned(K, 16) || !aligned(V, 16) || !aligned(seq, 4) || (pos && !aligned(pos, 4)))
         return HISA_E_INVAL;
     if (static_cast<long long>(n) * c->heads > INT_MAX) return HISA_E_UNSUPPORTED;
+    const unsigned long long bytes = 2ull * n * c->heads * c->d;
+    if (in_cache(c, K, bytes) || in_cache(c, V, bytes)) return HISA_E_INVAL;
     return HISA_OK;
 }
 
@@ -1415,7 +1426,7 @@ int hisa_rope(const hisa_rope_plan* plan, const uint16_t* x, uint16_t* y, const 
         return HISA_E_INVAL;
     if (rows == 0) return HISA_OK;
     if (!x || !y || !pos || !aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return HISA_E_INVAL;
-    if (x != y && overlap(x, y, 2ull * rows * heads * plan->d)) return HISA_E_INVAL;
+    if (x != y && overlap(x, 2ull * rows * heads * plan->d, y, 2ull * rows * heads * plan->d)) return HISA_E_INVAL;
     const int sms = sm_count();
     if (sms <= 0) return HISA_E_CUDA;
     RopeParams p;
@@ -1453,6 +1464,8 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
                     hisa_stream_t stream) {
     const int rc = check_cache_rows(c, K, V, seq, pos, n);
     if (rc || n == 0) return rc;
+    const unsigned long long bytes = 2ull * n * c->heads * c->d;
+    if (overlap(K, bytes, V, bytes)) return HISA_E_INVAL;
     CacheParams p = cache_params(c, seq, pos, n);
     p.k_out = K;
     p.v_out = V;
@@ -1485,7 +1498,8 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
         return HISA_E_INVAL;
     if (!ws || !aligned(ws, 256) || ws_bytes < need) return HISA_E_WORKSPACE;
     // a row's output may be written while another CTA has yet to read its queries
-    if (overlap(Qa, out, 2ull * n_q * Hq * c->d)) return HISA_E_INVAL;
+    const unsigned long long bytes = 2ull * n_q * Hq * c->d;
+    if (overlap(Qa, bytes, out, bytes)) return HISA_E_INVAL;
     const bool fp4 = c->dtype == HISA_CACHE_FP4;
     p.q = Qa;
     p.q_seq = q_seq;

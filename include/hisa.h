@@ -512,9 +512,11 @@ typedef struct hisa_attn_kv {
  * named twice holds afterwards is undefined (it may mix them).  K and V lie
  * outside the cache's own rows (in hisa_cache_load too).  A token with a
  * bad sequence (HISA_DEV_BAD_QUERY) or position (HISA_DEV_CAPACITY) is skipped.
- * hisa_cache_load — the way back: K, V [n, heads, d] bf16 out, the values the
- * cache's rows stand for; a zero row and a status bit for a bad name.
- * Errors: HISA_E_INVAL, HISA_E_UNSUPPORTED (d, cap), HISA_E_CUDA.
+ * hisa_cache_load — the way back: K, V [n, heads, d] bf16 out, which may not
+ * overlap one another, the values the cache's rows stand for; a zero row and a
+ * status bit for a bad name.
+ * Errors: HISA_E_INVAL (also rows inside the cache, and results that overlap),
+ * HISA_E_UNSUPPORTED (d, cap), HISA_E_CUDA.
  */
 int hisa_cache_store(const hisa_attn_kv* c, const uint16_t* K, const uint16_t* V, const int32_t* seq,
                      const int32_t* pos, int n, hisa_stream_t stream);

@@ -205,3 +205,40 @@ def test_lists_longer_than_the_plan_counts_are_refused():
             assert size(most) > 0
             for mb in (most + 1, (1 << 31) - 200, (1 << 31) - 1):
                 assert size(mb) == 0 and _attn(make(), Hq=Hq, n_q=1, mb=mb) == hisa.HISA_E_UNSUPPORTED, mb
+
+
+def _apart(make):
+    """A cache whose rows and scales lie apart: k from 16 MB on, v 32 MB further, the scales behind."""
+    mb = 1 << 20
+    over = dict(k=16 * mb, v=48 * mb, len=64, status=128)
+    if make is _fp4:
+        over.update(k_scale=80 * mb, v_scale=96 * mb)
+    return make(**over)
+
+
+def test_rows_inside_the_cache_are_refused():
+    mb, lib, free = 1 << 20, hisa.lib(), P(128 << 20)
+    size = 3 * 2 * 128 * 2                                       # n tokens of heads rows
+    for make in (_kv, _fp4):
+        c = _apart(make)
+        rows = 2 * 2 * 4096 * (256 if make is _kv else 64)
+        inside = [16 * mb, 16 * mb + rows - 16, 16 * mb - size + 16, 48 * mb, 48 * mb + rows - 16]
+        if make is _fp4:
+            scales = 2 * 2 * 4096 * 128 // 16
+            inside += [80 * mb, 80 * mb + scales - 16, 96 * mb - size + 16, 96 * mb + scales - 16]
+        for fn in (lib.hisa_cache_store, lib.hisa_cache_load):
+            for at in inside:
+                assert fn(ctypes.byref(c), P(at), free, P(64), None, 3, None) == hisa.HISA_E_INVAL, at
+                assert fn(ctypes.byref(c), free, P(at), P(64), None, 3, None) == hisa.HISA_E_INVAL, at
+
+
+def test_loaded_keys_and_values_that_overlap_are_refused():
+    """Where nothing overlaps the call goes on to the launch, which fails on a machine without a GPU."""
+    at, size, lib = 128 << 20, 3 * 2 * 128 * 2, hisa.lib()
+    for make in (_kv, _fp4):
+        c = _apart(make)
+        for v in (at, at + size - 16, at - size + 16):
+            assert lib.hisa_cache_load(ctypes.byref(c), P(at), P(v), P(64), None, 3, None) == hisa.HISA_E_INVAL, v
+        if not torch.cuda.is_available():                        # next to one another, and the same rows stored twice
+            for fn, v in ((lib.hisa_cache_load, at + size), (lib.hisa_cache_load, at - size), (lib.hisa_cache_store, at)):
+                assert fn(ctypes.byref(c), P(at), P(v), P(64), None, 3, None) == hisa.HISA_E_CUDA, v
