@@ -894,7 +894,7 @@ def hisa_block_attn(c: AttnCache, Qa: torch.Tensor, q_seq: torch.Tensor, q_pos: 
     """Attention of query rows Qa [n_q, Hq, d] bf16 over the tokens of their kept
     blocks [n_q, mb] of B tokens (blocks None: the whole prefix), up to each
     row's position.  Returns (out [n_q, Hq, d] bf16, lse [n_q, Hq] fp32); out
-    may not overlap Qa."""
+    and lse may not overlap Qa, the cache or one another."""
     fn, dev = "hisa_block_attn", c.device
     qp = _want(fn, "Qa", Qa, torch.bfloat16, dev, (-1, -1, c.d))
     n_q, Hq, d = Qa.shape

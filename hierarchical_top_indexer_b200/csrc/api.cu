@@ -1497,9 +1497,11 @@ int hisa_block_attn(const hisa_attn_kv* c, const uint16_t* Qa, int Hq, const int
         (q_pos && !aligned(q_pos, 4)) || (blocks && !aligned(blocks, 4)) || (lse && !aligned(lse, 4)))
         return HISA_E_INVAL;
     if (!ws || !aligned(ws, 256) || ws_bytes < need) return HISA_E_WORKSPACE;
-    // a row's output may be written while another CTA has yet to read its queries
-    const unsigned long long bytes = 2ull * n_q * Hq * c->d;
-    if (overlap(Qa, bytes, out, bytes)) return HISA_E_INVAL;
+    // a row's output may be written while another CTA has yet to read its queries or its keys
+    const unsigned long long bytes = 2ull * n_q * Hq * c->d, lse_bytes = 4ull * n_q * Hq;
+    if (overlap(Qa, bytes, out, bytes) || in_cache(c, out, bytes)) return HISA_E_INVAL;
+    if (lse && (overlap(Qa, bytes, lse, lse_bytes) || overlap(out, bytes, lse, lse_bytes) || in_cache(c, lse, lse_bytes)))
+        return HISA_E_INVAL;
     const bool fp4 = c->dtype == HISA_CACHE_FP4;
     p.q = Qa;
     p.q_seq = q_seq;

@@ -540,8 +540,8 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  *          output of hisa_select_blocks or hisa_select_inspect); entries that
  *          are negative or lie past the row's position are skipped, a repeated
  *          id counts once.  NULL with mb = 0: the whole prefix (B is not read)
- *   out    [n_q, Hq, d] bf16, which may not overlap Qa; lse [n_q, Hq] fp32 or
- *          NULL
+ *   out    [n_q, Hq, d] bf16; lse [n_q, Hq] fp32 or NULL; neither may overlap
+ *          the other, Qa or the cache's rows
  *   ws     workspace of at least hisa_block_attn_workspace_bytes(...) bytes
  * A row that sees no token gives out = 0 and lse = -inf; a row whose position
  * is not inside its prefix does too, and sets HISA_DEV_BAD_QUERY.  Sizes: B as

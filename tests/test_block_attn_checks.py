@@ -242,3 +242,19 @@ def test_loaded_keys_and_values_that_overlap_are_refused():
         if not torch.cuda.is_available():                        # next to one another, and the same rows stored twice
             for fn, v in ((lib.hisa_cache_load, at + size), (lib.hisa_cache_load, at - size), (lib.hisa_cache_store, at)):
                 assert fn(ctypes.byref(c), P(at), P(v), P(64), None, 3, None) == hisa.HISA_E_CUDA, v
+
+
+def test_outputs_that_overlap_each_other_or_the_cache_are_refused():
+    mb, size, lse = 1 << 20, 4 * 16 * 128 * 2, 4 * 16 * 4           # n_q rows of Hq heads
+    at, far = 128 * mb, 256 * mb
+    for make in (_kv, _fp4):
+        c = _apart(make)
+        call = lambda **kw: _attn(c, **{**dict(Qa=P(at), out=P(far), lse=P(64 * mb + far)), **kw})  # noqa: E731,B023
+        for x in (at, at + size - 4, at - lse + 4):
+            assert call(lse=P(x)) == hisa.HISA_E_INVAL, x
+        for x in (far, far + size - 4, far - lse + 4):
+            assert call(lse=P(x)) == hisa.HISA_E_INVAL, x
+        for x in (16 * mb, 48 * mb) + (() if make is _kv else (80 * mb, 96 * mb)):
+            assert call(out=P(x)) == call(out=P(x - size + 16)) == call(lse=P(x)) == call(lse=P(x - 4)) == hisa.HISA_E_INVAL
+        if not torch.cuda.is_available():                        # next to one another: the call goes on to the device
+            assert call(lse=P(far + size)) == call(lse=P(at - lse)) == call(lse=None) == hisa.HISA_E_CUDA
