@@ -1413,7 +1413,7 @@ int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, do
     plan->off = off;
     plan->layout = layout;
     plan->gain = static_cast<float>(gain != 0.0 ? gain : scaling == HISA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0);
-    if (!std::isfinite(plan->gain)) return HISA_E_INVAL;
+    if (!std::isnormal(plan->gain)) return HISA_E_INVAL;
     plan->ready = 1;
     return HISA_OK;
 }

@@ -428,7 +428,8 @@ int hisa_select_blocks(const hisa_kv* kv, const uint16_t* Q, const float* w, con
  *                    lo = max(floor(c(beta_fast)), 0) and
  *                    hi = min(ceil(c(beta_slow)), rot - 1), where
  *                    c(t) = rot ln(orig_len / (2 pi t)) / (2 ln base)
- *   gain     g, in fp32's range; 0: the scaling's own, 0.1 ln(factor) + 1 for YARN, else 1
+ *   gain     g, a normal number of fp32; 0: the scaling's own, 0.1 ln(factor) + 1
+ *            for YARN, else 1
  * factor >= 1; base > 1; YARN: orig_len > 0, beta_fast >= beta_slow > 0.
  * Angles are exact to about 2^-31 of a turn at every 32-bit position,
  * negative ones included.

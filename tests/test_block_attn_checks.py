@@ -258,3 +258,13 @@ def test_outputs_that_overlap_each_other_or_the_cache_are_refused():
             assert call(out=P(x)) == call(out=P(x - size + 16)) == call(lse=P(x)) == call(lse=P(x - 4)) == hisa.HISA_E_INVAL
         if not torch.cuda.is_available():                        # next to one another: the call goes on to the device
             assert call(lse=P(far + size)) == call(lse=P(at - lse)) == call(lse=None) == hisa.HISA_E_CUDA
+
+
+def test_a_gain_below_fp32_is_refused():
+    """It would come out as 0 (or lose bits), which as an argument stands for the scaling's own gain."""
+    for gain in (1e-46, -1e-60, 1e-39):
+        with pytest.raises(hisa.HisaError) as e:
+            hisa.hisa_rope_init(64, gain=gain)
+        assert e.value.code == hisa.HISA_E_INVAL
+    for gain in (2.0 ** -126, -3.0, 3e38):
+        assert hisa.hisa_rope_init(64, gain=gain).gain == torch.tensor(gain, dtype=torch.float32).item()
