@@ -1421,8 +1421,9 @@ int hisa_rope_init(hisa_rope_plan* plan, int d, int rot, int off, int layout, do
 int hisa_rope(const hisa_rope_plan* plan, const uint16_t* x, uint16_t* y, const int32_t* pos, int rows, int heads,
               int transpose, hisa_stream_t stream) {
     if (!plan || plan->ready != 1 || rows < 0 || heads < 1 || heads > 1 << 16) return HISA_E_INVAL;
-    if (plan->rot < 2 || plan->rot > 2 * HISA_ROPE_MAX_PAIRS || plan->d < plan->rot || plan->d > 512 || plan->off < 0 ||
-        plan->off > plan->d - plan->rot)
+    if (plan->rot < 2 || plan->rot % 2 != 0 || plan->rot > 2 * HISA_ROPE_MAX_PAIRS || plan->d < plan->rot || plan->d > 512 ||
+        plan->off < 0 || plan->off > plan->d - plan->rot ||
+        (plan->layout != HISA_ROPE_HALF && plan->layout != HISA_ROPE_INTERLEAVED))
         return HISA_E_INVAL;
     if (rows == 0) return HISA_OK;
     if (!x || !y || !pos || !aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return HISA_E_INVAL;

@@ -268,3 +268,13 @@ def test_a_gain_below_fp32_is_refused():
         assert e.value.code == hisa.HISA_E_INVAL
     for gain in (2.0 ** -126, -3.0, 3e38):
         assert hisa.hisa_rope_init(64, gain=gain).gain == torch.tensor(gain, dtype=torch.float32).item()
+
+
+@pytest.mark.parametrize("field,value", [("d", 62), ("d", 513), ("rot", 0), ("rot", 63), ("rot", 258), ("off", -1), ("off", 1),
+                                         ("layout", 2), ("layout", -1), ("ready", 0), ("ready", 2)])
+def test_a_plan_that_was_written_over_is_refused(field, value):
+    """A plan is plain memory; one whose sizes or layout hisa_rope_init would have refused is refused by the call too
+    (an odd rot left an element of y unwritten, an unknown layout ran as HALF)."""
+    p = hisa.hisa_rope_init(64)
+    setattr(p, field, value)
+    assert hisa.lib().hisa_rope(ctypes.byref(p), P(16), P(16), P(16), 4, 2, 0, None) == hisa.HISA_E_INVAL
