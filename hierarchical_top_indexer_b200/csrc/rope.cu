@@ -8,9 +8,11 @@
 // as a fraction of a turn in 64-bit fixed point: turns_i = w_i / 2 pi * 2^64,
 // and p * turns_i modulo 2^64 drops whole turns exactly, so a position of a
 // million is as exact as position 1 (an fp32 product p * w_i would be off by
-// 2^-24 p radians, 0.06 at a million).  The top 32 bits of the fraction go
-// through sincospi in fp32 (about 2^-24 of a turn), the rotation is computed
-// in fp32 and rounded once to bf16.
+// 2^-24 p radians, 0.06 at a million).  The fraction is rounded to 32 bits
+// (2^-33 of a turn; the rounding of turns_i adds up to 2^-34 at the farthest
+// positions) and then to fp32's 24 for sincospi (up to 2^-26 of a turn, in
+// the outer half of [-1/2, 1/2]); the rotation is computed in fp32 and rounded
+// once to bf16.
 //
 // Bound: 4 bytes per element (read once, written once).  A block takes a few
 // rows and all or some of their heads; it issues its loads first (up to four

@@ -431,8 +431,9 @@ int hisa_select_blocks(const hisa_kv* kv, const uint16_t* Q, const float* w, con
  *   gain     g, a normal number of fp32; 0: the scaling's own, 0.1 ln(factor) + 1
  *            for YARN, else 1
  * factor >= 1; base > 1; YARN: orig_len > 0, beta_fast >= beta_slow > 0.
- * Angles are exact to about 2^-31 of a turn at every 32-bit position,
- * negative ones included.
+ * At every 32-bit position, negative ones included, the angle modulo a turn is
+ * off by up to 2^-32 of a turn before it is rounded to fp32, which adds up to
+ * 2^-26 of a turn; fp32's sine and cosine follow.
  */
 #define HISA_ROPE_MAX_PAIRS 128
 enum hisa_rope_layout { HISA_ROPE_HALF = 0, HISA_ROPE_INTERLEAVED = 1 };
