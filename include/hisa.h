@@ -506,7 +506,9 @@ typedef struct hisa_attn_kv {
  *   seq    [n] int32 sequence of each token
  *   pos    [n] int32 position of each token in 0 .. cap - 1; NULL: each
  *          sequence's last position len[seq] - 1 (a decode step: after
- *          hisa_append or hisa_decode_step has advanced the shared len)
+ *          hisa_append or hisa_decode_step has advanced the shared len; of a
+ *          sequence that was full, and whose len they left as it was, the last
+ *          row is written again: leave such a token out, or name positions)
  * Reads len only for pos = NULL and never changes it.  FP4 rows are
  * quantised: per 16 elements scale = e4m3(min(448, max|x| / (6 mul))), code =
  * e2m1(x / (mul * scale)), both to nearest with ties to even, codes saturated
