@@ -39,10 +39,14 @@
 // all their bits and only those below 2^-32 of it vanish.
 //
 // Bound (d = 128): 4096 rows of one sequence, 64 of 256 blocks each, 16 heads
-// over 2 key heads, 676 us: about 2400 cycles a tile, of which the 2^x unit
-// takes 1024 and the MMAs 1024; the rest is the chain of each set (S, softmax,
-// P V), because P takes S's place and the next S of the set waits for P V.
-// 4-bit rows, 2 x 512 rows causal over 8191 keys, 32 heads over 4: 213 us.
+// over 2 key heads, 681 to 743 us: 2500 to 2700 cycles a tile, of which the 2^x
+// unit takes 1024 and the MMAs 1024; the rest is the chain of each set (S,
+// softmax, P V), because P takes S's place and the next S of the set waits for
+// P V, and the softmax's registers: at 168 a thread it reads S twice and spills
+// (352 bytes stored, 580 loaded).  4-bit rows, 2 x 512 rows causal over 8191
+// keys, 32 heads over 4: 223 to 227 us; the same over bf16 rows 186 us, and
+// 182 us without the expansion, whose four warps do K and then V of a tile
+// (216 and 484 bytes of spills at 128 registers).
 // An element-wise mask costs twice the whole tile, hence the rows that are on
 // or off; a single polling lane per wait cost twice the kernel (1459 us).
 #include "battn.cuh"
@@ -874,12 +878,24 @@ cudaError_t launch_typed(const CUtensorMap& qm, const CUtensorMap& km, const CUt
 
 size_t battn_layout(BattnParams& p, void* ws) {
     // Groups of rows where there are more rows than sequences.  Over whole prefixes a group
-    // reads what each of its rows would (8 sequences of 32K keys, G = 8: 2 rows each 83 us in
-    // groups, 93 us alone; 4 rows 78 and 159 us).  Over kept blocks it reads their union, which
-    // pays with some rows to a group and some groups (64 kept of 256 blocks, G = 8, R = 16: 64
-    // rows of one sequence 62 us in groups, 54 us alone; 128 rows 79 and 87 us; 4096 rows 676
-    // and 2105 us; 9 rows of 8 sequences 86 and 62 us, 32 rows of 8 104 and 166 us), and where
-    // the kernel for lone rows does not serve (64 rows of G = 32: 72 and 92 us).
+    // reads once what each of its rows would; over kept blocks it reads their union, which
+    // pays with some rows to a group and some groups, and where the kernel for lone rows does
+    // not serve (64 rows of G = 32: 72 and 92 us).  In groups and alone, us a call:
+    //   whole prefixes, 8 sequences of 32K keys, 2 key heads, G = 8, rows of each
+    //                      2          3          4          8
+    //     bf16          81  89     85 116     78 158     84 255     (G = 1: 2 rows 76  86)
+    //     4 bits        77  57     80  75     74  92     78 165     (G = 1: 2 rows 71  53)
+    //   64 kept of 256 blocks of 128, one sequence, 2 key heads, rows
+    //                     64         96        128        192        512
+    //     bf16, G = 8   59  54     69  69     76  85     80 117    129 277   (4096: 676 2105)
+    //     bf16, G = 1   62  51     76  67     88  83     90 115    116 274
+    //     4 bits, G = 8 58  63     69  82     78 101     84 139    146 337
+    //     4 bits, G = 1 63  59     77  79     93  98    102 137    117 333
+    //   8 sequences, bf16, G = 8: 9 rows of each 86 and 62, 32 rows 104 and 166
+    //   256 kept of 2048 blocks of 16, bf16, G = 8: 96 rows 81 and 53, 256 rows 125 and 112
+    //   (4 bits 80 and 84, 116 and 188)
+    // The rule takes the slower side for two or three 4-bit rows over a whole prefix, for bf16
+    // chunks of a few hundred rows over small blocks, and at G = 1 from about 130 to 255 rows.
     p.G = p.Hq / p.Hkv;
     const bool sparse = p.mb > 0;
     const int most = 128 / p.G;

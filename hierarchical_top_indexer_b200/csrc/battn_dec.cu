@@ -31,11 +31,12 @@
 // six 18 KB stages of rows, four K buffers, three V tiles.
 //
 // Bound (d = 128): bf16 rows by HBM, 64 rows of 8192 kept keys and 8 key heads
-// in 338 us, 6.4 TB/s.  4-bit rows: 16 prefixes of about 115K keys and 4 key
-// heads in 278 to 300 us, 3.7 TB/s; 211 us of it remain when neither the
-// expanding nor the softmax does anything, so the hand-over from stage to
-// stage bounds it (shared memory moves about 110 KB a tile, 860 of the 1360
-// cycles a tile takes).
+// in 338 to 342 us, 6.3 TB/s.  4-bit rows: 16 prefixes of about 115K keys and 4
+// key heads in 279 to 302 us, 3.5 to 3.8 TB/s; 211 us of 277 remained when
+// neither the expanding nor the softmax did anything, so the hand-over from
+// stage to stage bounds it (shared memory moves about 110 KB a tile, 860 of the
+// 1400 cycles a tile takes).  At 80 registers for 23 warps it spills 140 bytes
+// (312 loaded); bf16 rows have 114 and spill none.
 #include "battn.cuh"
 
 namespace hisa {

@@ -15,7 +15,12 @@
 // Bound: 2 bytes read and 0.5625 written per element (store; load the other
 // way).  One thread per group of the keys and the same of the values: four
 // 16-byte loads in flight before it knows its row, two 8-byte stores of codes
-// and two bytes of scale; the groups of a row are neighbouring threads.
+// and two bytes of scale; the groups of a row are neighbouring threads.  16384
+// tokens of 8 heads of 128 at a random half of the positions, keys and values:
+// 4 bits stored in 17.0 us and loaded in 20.0 us (at contiguous positions 16.5
+// and 18.7: a token's heads lie apart, so a row is 64 bytes of codes and 8 of
+// scales), bf16 21.9 and 23.4 us; both run in turn over other inputs take 40.4
+// us for 4 bits, 66% of the measured copy rate.
 #include "hisa_kernels.cuh"
 
 namespace hisa {

@@ -18,9 +18,10 @@
 // rows and all or some of their heads; it issues its loads first (up to four
 // tasks of one or two 16-byte chunks per thread), computes the sine and cosine
 // of each (row, pair) once while they are in flight, and every head of the
-// row uses them.  4096 rows of 64 heads of 128, 64 of them rotated: 24.7 us,
-// 84% of the measured copy rate; with 256 threads a block 27.0 us, with 64
-// threads of eight tasks 31.6 us (small blocks load while others store).
+// row uses them.  4096 rows of 64 heads of 128, 64 of them rotated: 24.5 to
+// 26.1 us, 80 to 85% of the measured copy rate.  With 256 threads a block 27.0
+// us and with 64 threads of eight tasks 31.6 us where this took 24.7 (small
+// blocks load while others store).
 #include "hisa_kernels.cuh"
 
 namespace hisa {
