@@ -555,7 +555,9 @@ int hisa_cache_load(const hisa_attn_kv* c, uint16_t* K, uint16_t* V, const int32
  * fp32, whose range those of the tokens a row sees must stay in (another
  * row's may leave it); softmax maxima and sums in fp32; the weights are
  * rounded to bf16 (f16 for FP4 rows) for the product with the values,
- * accumulated in fp32; out is rounded once to bf16.  Results do not depend on
+ * accumulated in fp32; out is rounded once to bf16.  The sums before the
+ * division hold weights of up to 2^8, so that bf16 values of up to 2^88 cannot
+ * overflow them at any length, and larger ones may.  Results do not depend on
  * the order of atomics.
  * Errors: HISA_E_INVAL, HISA_E_UNSUPPORTED, HISA_E_WORKSPACE, HISA_E_CUDA.
  */

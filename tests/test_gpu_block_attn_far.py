@@ -56,3 +56,22 @@ def test_select_then_attend_with_no_rows(dtype):
         out, lse = hisa.hisa_block_attn(c, Qa[:0], none, pos, blocks, B=64)
         assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
     assert kv.status_bits() == 0
+
+
+@pytest.mark.parametrize("d,G,rows", [(128, 8, 1), (128, 8, 40), (64, 5, 1), (64, 20, 1), (64, 1, 140)])
+def test_values_as_large_as_the_header_allows(d, G, rows):
+    """Values around 2^87, weights of rows whose maximum keeps growing a little: the sums before the division are up to
+    2^8 times the values and the number of tokens."""
+    rng = np.random.default_rng(d + G)
+    batch, cap, Hkv = 2, 2048, 2
+    K, V = rng.standard_normal((2, batch, Hkv, cap, d))
+    K += np.linspace(0, 6, cap)[:, None] / math.sqrt(d)
+    V = np.clip(V, -4, 4) * 2.0 ** 86
+    Q = 1 + 0.2 * rng.standard_normal((batch * rows, Hkv * G, d))
+    seq, pos = np.repeat([0, 1], rows), np.tile(np.arange(cap - rows, cap), 2)
+    k, v, q = _bf(K), _bf(V), _bf(Q)
+    c = hisa.AttnCache.wrap(k, v, _i32([cap, cap]))
+    out, lse = hisa.hisa_block_attn(c, q, _i32(seq), _i32(pos))
+    assert torch.isfinite(out.float()).all() and float(v.float().abs().max()) <= 2.0 ** 88
+    r = ref.block_attn(_f64(q), _f64(k), _f64(v), seq, pos, None, 1, 1 / math.sqrt(d))
+    ref.check_block_attn(_f64(out), _f64(lse), r, d, False)
